@@ -64,6 +64,35 @@ int ddt_drafter_topk(const void* logits, int logits_dtype, int V, int R, int K, 
   return ddt::launch_drafter_topk(p, stream);
 }
 
+int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_stride, const int32_t* nodes,
+                       const int32_t* tok, int B, int N, int M, int K, float* logp, float* entropy, float* top_logp,
+                       int32_t* top_tok, int32_t* dev_status, cudaStream_t stream) {
+  if (!logits || !tok || !logp) return DDT_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || M < 1 || V < 1 || K < 0 || K > 32 || K > V || row_stride < V) return DDT_ERR_INVALID_ARG;
+  if (K > 0 && (!top_logp || !top_tok)) return DDT_ERR_INVALID_ARG;
+  if (!nodes && M > N) return DDT_ERR_INVALID_ARG;
+  if (logits_dtype != DDT_F32 && logits_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
+  if (!ddt::aligned(logits, logits_dtype == DDT_F32 ? 4 : 2)) return DDT_ERR_INVALID_ARG;
+  if ((long long)B * M > 0x7fffffffLL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
+  ddt::LogprobsParams p{};
+  p.logits = logits;
+  p.logits_dtype = logits_dtype;
+  p.V = V;
+  p.row_stride = row_stride;
+  p.B = B;
+  p.N = N;
+  p.M = M;
+  p.K = K;
+  p.nodes = nodes;
+  p.tok = tok;
+  p.logp = logp;
+  p.entropy = entropy;
+  p.top_logp = top_logp;
+  p.top_tok = top_tok;
+  p.dev_status = dev_status;
+  return ddt::launch_token_logprobs(p, stream);
+}
+
 int ddt_build_tree(const float* logp, const int32_t* tok, const int32_t* root_tok,
                    const int32_t* cache_len, int B, int D, int K, int N, int32_t* node_tok,
                    int32_t* parent, int32_t* depth, int32_t* pos, float* score, uint32_t* mask,

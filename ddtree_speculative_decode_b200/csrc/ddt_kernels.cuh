@@ -80,6 +80,26 @@ struct DrafterParams {
 };
 int launch_drafter_topk(DrafterParams p, cudaStream_t stream);
 
+// ---- log probabilities of given tokens ------------------------------------------
+struct LogprobsParams {
+  const void* logits;     // [B][N] rows, row_stride elements apart
+  int logits_dtype;
+  int V;
+  int64_t row_stride;
+  int B, N, M, K;
+  const int32_t* nodes;   // [B][M], nullable: entry j is node j
+  const int32_t* tok;     // [B][M]
+  float* logp;            // [B][M]
+  float* entropy;         // [B][M], nullable
+  float* top_logp;        // [B][M][K]
+  int32_t* top_tok;       // [B][M][K]
+  int32_t* dev_status;    // [B][M], nullable
+  int64_t e0;             // first entry of this launch
+  int R;                  // entries of this launch
+  int cluster;            // CTAs per cluster
+};
+int launch_token_logprobs(LogprobsParams p, cudaStream_t stream);
+
 // ---- verify attention -------------------------------------------------------
 struct AttnParams {
   const void* q;

@@ -34,6 +34,7 @@ EXPORTS = (
     "ddt_accept_compact_noalloc",
     "ddt_accept_compact_lmhead",
     "ddt_drafter_topk",
+    "ddt_token_logprobs",
 )
 
 _lib = None
@@ -82,6 +83,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                               vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.ddt_drafter_topk.restype = i32
     lib.ddt_drafter_topk.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    lib.ddt_token_logprobs.restype = i32
+    lib.ddt_token_logprobs.argtypes = [vp, i32, i32, i64, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     if path is None:
         _lib = lib
     return lib
@@ -412,4 +415,62 @@ def accept_compact_lmhead(hidden: torch.Tensor, w_vocab: torch.Tensor, node_tok:
             _ptr(out["out_tok"]), _ptr(out["bonus"]), _ptr(out["status"]), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream(stream))
     _raise("ddt_accept_compact_lmhead", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# token scores
+# ---------------------------------------------------------------------------
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a [B, N, V] tensor whose rows are
+    contiguous and evenly spaced (a slice of padded rows is)."""
+    B, N, V = t.shape
+    sb, sn, sv = t.stride()
+    if V > 1 and sv != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    step = sn if N > 1 else sb if B > 1 else V
+    if (B > 1 and N > 1 and sb != N * sn) or step < V:
+        raise ValueError(f"{name}: rows must be evenly spaced and must not overlap")
+    return step
+
+
+def alloc_logprobs(B: int, M: int, K: int, device) -> dict:
+    f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+    return {"logp": torch.empty(B, M, **f32), "entropy": torch.empty(B, M, **f32),
+            "top_logp": torch.empty(B, M, K, **f32), "top_tok": torch.empty(B, M, K, **i32),
+            "status": torch.empty(B, M, **i32)}
+
+
+def token_logprobs(logits: torch.Tensor, tok: torch.Tensor, nodes: Optional[torch.Tensor] = None, K: int = 0,
+                   out: Optional[dict] = None, stream=None) -> dict:
+    """ddt_token_logprobs. logits [B, N, V] f32 / bf16 (rows contiguous and
+    evenly spaced: padded rows may be sliced), tok [B, M] i32, nodes [B, M] i32
+    (None: entry j is row j; negative entries are skipped) -- accept_compact's
+    out_tok and acc_nodes, or any other tokens and rows. Returns logp, entropy
+    [B, M] f32, top_logp [B, M, K] f32, top_tok [B, M, K] i32, status [B, M]."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits: must be a CUDA tensor")
+    dt = _dt(logits)
+    if logits.dim() != 3 or tok.dim() != 2:
+        raise ValueError("expected logits [B, N, V] and tok [B, M]")
+    B, N, V = logits.shape
+    step = _row_stride(logits, "logits")
+    M = tok.shape[1]
+    _check(tok, "tok", torch.int32, (B, M))
+    if nodes is not None:
+        _check(nodes, "nodes", torch.int32, (B, M))
+    if out is None:
+        out = alloc_logprobs(B, M, K, logits.device)
+    f32, i32 = torch.float32, torch.int32
+    _check_out(out, {"logp": (f32, (B, M)), "entropy": (f32, (B, M)), "top_logp": (f32, (B, M, K)),
+                     "top_tok": (i32, (B, M, K)), "status": (i32, (B, M))})
+    with _device(logits, tok, nodes, *out.values(), stream=stream):
+        st = load().ddt_token_logprobs(_ptr(logits), dt, V, step, _ptr(nodes), _ptr(tok), B, N, M, K,
+                                       _ptr(out["logp"]), _ptr(out["entropy"]), _ptr(out["top_logp"]),
+                                       _ptr(out["top_tok"]), _ptr(out["status"]), _stream(stream))
+    _raise("ddt_token_logprobs", st)
     return out

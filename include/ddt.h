@@ -398,6 +398,49 @@ DDT_API int ddt_accept_compact_noalloc(const void* logits, int logits_dtype, int
                                        int32_t* am, int32_t* acc_len, int32_t* acc_nodes, int32_t* out_tok,
                                        int32_t* bonus, int32_t* dev_status, cudaStream_t stream);
 
+/*
+ * ddt_token_logprobs -- log probabilities of given tokens at selected verify
+ * rows, with each row's entropy and its K most likely tokens: what a server
+ * reports beside the tokens ddt_accept_compact commits (tok = out_tok at
+ * nodes = acc_nodes), or the score of a given text (nodes null).
+ *
+ * No counterpart on the pages: they stop at the greedy tokens.
+ *
+ * Definition: entry (b, j) reads row x = logits[b][node] with node =
+ *   nodes[b][j] (nodes null: node = j), as softmax logits, p_v = e^x_v / sum_w
+ *   e^x_w over the whole vocabulary:
+ *   logp[b][j]    = ln p_t for t = tok[b][j];
+ *   entropy[b][j] = -sum_v p_v ln p_v (0 ln 0 = 0);
+ *   top_tok[b][j][k] = the k-th most likely token (equal logits: the lower
+ *                 token first), top_logp[b][j][k] = its ln p.
+ *   A logit of -inf is a token that cannot be drawn: p = 0, never among the
+ *   alternatives (entries beyond the last possible token: -1, -inf), and
+ *   logp = -inf where it is the given token. float32 arithmetic, relative to
+ *   the row's largest logit: rows of the type's lowest values are exact too.
+ *   Results do not depend on how the rows are split, up to rounding, and are
+ *   the same on every run of the same call on the same device.
+ * Inputs (device): logits: rows of V logits_dtype values (F32 or BF16),
+ *   row (b, i) at element (b * N + i) * row_stride (row_stride >= V: rows may
+ *   be padded), aligned to the element; nodes [B][M] int32 (nullable; a
+ *   negative entry is skipped), tok [B][M] int32 (not read for skipped ones).
+ * Outputs (device): logp [B][M] float32; entropy [B][M] float32 (nullable);
+ *   top_logp [B][M][K] float32 and top_tok [B][M][K] int32 (not used for K =
+ *   0); dev_status [B][M] int32 (nullable).
+ *   Skipped entries: logp 0, entropy 0, top -inf / -1, DDT_OK.
+ *   DDT_ERR_INPUT: node >= N, a token outside [0, V), or a row with a NaN, a
+ *   +inf or no finite logit -- that entry gets logp -inf, entropy 0, top
+ *   -inf / -1.
+ * Sizes: B, N, M, V >= 1, 0 <= K <= min(V, 32), M <= N when nodes is null;
+ *   B * M < 2^31 and V <= 2^30 (DDT_ERR_UNSUPPORTED beyond).
+ * Every selected row is read once; rows that no entry selects are not read.
+ *   One launch (one per 4096 entries when nodes is given); no workspace.
+ *   Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, alignment),
+ *   DDT_ERR_UNSUPPORTED, DDT_ERR_CUDA (launch).
+ */
+DDT_API int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_stride, const int32_t* nodes,
+                               const int32_t* tok, int B, int N, int M, int K, float* logp, float* entropy,
+                               float* top_logp, int32_t* top_tok, int32_t* dev_status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
