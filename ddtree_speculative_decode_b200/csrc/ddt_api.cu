@@ -93,6 +93,56 @@ int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_
   return ddt::launch_token_logprobs(p, stream);
 }
 
+size_t ddt_cache_evict_workspace_size(int B, int n_layers, int max_cache_len) {
+  if (B < 1 || n_layers < 1 || max_cache_len < 0) return 0;
+  return ddt::evict_workspace_bytes(B, n_layers, max_cache_len);
+}
+
+int ddt_cache_evict(void* kv, int64_t kv_rows, int kv_dtype, int row_elems, float* score, int n_layers,
+                    int64_t layer_stride_rows, const int64_t* cache_off, const int32_t* cache_len,
+                    const int32_t* keep, int sink, int recent, int B, int max_cache_len, void* kv_dst,
+                    int64_t dst_rows, float* score_dst, int64_t dst_layer_stride_rows, const int64_t* dst_off,
+                    int32_t* new_len, int32_t* src, int max_keep, int32_t* dev_status, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream) {
+  if (!kv || !score || !cache_off || !cache_len || !keep || !new_len || !src || !workspace) return DDT_ERR_INVALID_ARG;
+  if ((kv_dst != nullptr) != (score_dst != nullptr) || (kv_dst != nullptr) != (dst_off != nullptr))
+    return DDT_ERR_INVALID_ARG;
+  if (B < 1 || n_layers < 1 || row_elems < 1 || kv_rows < 1 || layer_stride_rows < 0 || sink < 0 || recent < 0 ||
+      max_cache_len < 0 || max_keep < 1)
+    return DDT_ERR_INVALID_ARG;
+  if (n_layers > 1 && (layer_stride_rows < 1 || (kv_dst && dst_layer_stride_rows < 1))) return DDT_ERR_INVALID_ARG;
+  if (kv_dst && (kv_dst == kv || dst_rows < 1 || dst_layer_stride_rows < 0)) return DDT_ERR_INVALID_ARG;
+  if (kv_dtype != DDT_F32 && kv_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
+  const long long row_bytes = (long long)row_elems * (kv_dtype == DDT_F32 ? 4 : 2);
+  if (row_bytes % 4 != 0 || row_bytes > (1 << 20)) return DDT_ERR_INVALID_ARG;
+  if (!ddt::aligned(kv, 4) || !ddt::aligned(kv_dst, 4) || !ddt::aligned(workspace, 256)) return DDT_ERR_INVALID_ARG;
+  if (workspace_bytes < ddt::evict_workspace_bytes(B, n_layers, max_cache_len)) return DDT_ERR_INVALID_ARG;
+  if ((long long)B * n_layers > 0x7fffffffLL) return DDT_ERR_UNSUPPORTED;
+  ddt::EvictParams p{};
+  p.kv = kv;
+  p.kv_rows = kv_rows;
+  p.row_bytes = (int)row_bytes;
+  p.score = score;
+  p.n_layers = n_layers;
+  p.layer_stride_rows = layer_stride_rows;
+  p.cache_off = cache_off;
+  p.cache_len = cache_len;
+  p.keep = keep;
+  p.sink = sink;
+  p.recent = recent;
+  p.B = B;
+  p.kv_dst = kv_dst;
+  p.dst_rows = dst_rows;
+  p.score_dst = score_dst;
+  p.dst_layer_stride_rows = dst_layer_stride_rows;
+  p.dst_off = dst_off;
+  p.new_len = new_len;
+  p.src = src;
+  p.max_keep = max_keep;
+  p.dev_status = dev_status;
+  return ddt::launch_cache_evict(p, max_cache_len, workspace, stream);
+}
+
 int ddt_build_tree(const float* logp, const int32_t* tok, const int32_t* root_tok,
                    const int32_t* cache_len, int B, int D, int K, int N, int32_t* node_tok,
                    int32_t* parent, int32_t* depth, int32_t* pos, float* score, uint32_t* mask,

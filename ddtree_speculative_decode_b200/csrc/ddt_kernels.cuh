@@ -100,6 +100,34 @@ struct LogprobsParams {
 };
 int launch_token_logprobs(LogprobsParams p, cudaStream_t stream);
 
+// ---- eviction of cache rows ------------------------------------------------------
+struct EvictParams {
+  void* kv;
+  int64_t kv_rows;
+  int row_bytes;
+  float* score;               // one per pool row
+  int n_layers;
+  int64_t layer_stride_rows;
+  const int64_t* cache_off;
+  const int32_t* cache_len;
+  const int32_t* keep;        // [B]
+  int sink, recent, B;
+  void* kv_dst;               // null: in place
+  int64_t dst_rows;
+  float* score_dst;
+  int64_t dst_layer_stride_rows;
+  const int64_t* dst_off;
+  int32_t* new_len;           // [B]; may be cache_len
+  int32_t* src;               // [n_layers][B][max_keep]
+  int max_keep;
+  int32_t* dev_status;        // [B], nullable
+  int2* plan;                 // [n_layers][B]: rows kept (-1: skipped), first row that moves
+  int held_keys;              // keys that fit the selection's shared memory
+  int row_vecs, block_rows, blocks, col;  // the copy's split
+};
+size_t evict_workspace_bytes(int B, int n_layers, int max_cache_len);
+int launch_cache_evict(EvictParams p, int max_cache_len, void* workspace, cudaStream_t stream);
+
 // ---- verify attention -------------------------------------------------------
 struct AttnParams {
   const void* q;

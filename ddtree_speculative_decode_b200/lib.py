@@ -35,6 +35,8 @@ EXPORTS = (
     "ddt_accept_compact_lmhead",
     "ddt_drafter_topk",
     "ddt_token_logprobs",
+    "ddt_cache_evict_workspace_size",
+    "ddt_cache_evict",
 )
 
 _lib = None
@@ -85,6 +87,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ddt_drafter_topk.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.ddt_token_logprobs.restype = i32
     lib.ddt_token_logprobs.argtypes = [vp, i32, i32, i64, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.ddt_cache_evict_workspace_size.restype = sz
+    lib.ddt_cache_evict_workspace_size.argtypes = [i32, i32, i32]
+    lib.ddt_cache_evict.restype = i32
+    lib.ddt_cache_evict.argtypes = [vp, i64, i32, i32, vp, i32, i64, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i64,
+                                    vp, vp, vp, i32, vp, vp, sz, vp]
     if path is None:
         _lib = lib
     return lib
@@ -473,4 +480,73 @@ def token_logprobs(logits: torch.Tensor, tok: torch.Tensor, nodes: Optional[torc
                                        _ptr(out["logp"]), _ptr(out["entropy"]), _ptr(out["top_logp"]),
                                        _ptr(out["top_tok"]), _ptr(out["status"]), _stream(stream))
     _raise("ddt_token_logprobs", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# cache budget
+# ---------------------------------------------------------------------------
+
+
+def cache_evict_workspace_size(B: int, n_layers: int, max_cache_len: int) -> int:
+    return int(load().ddt_cache_evict_workspace_size(B, n_layers, max_cache_len))
+
+
+def cache_evict(kv: torch.Tensor, score: torch.Tensor, cache_off: torch.Tensor, cache_len: torch.Tensor,
+                keep: torch.Tensor, sink: int, recent: int, max_cache_len: int, n_layers: int = 1,
+                layer_stride_rows: int = 0, dst: Optional[dict] = None, max_keep: Optional[int] = None,
+                out: Optional[dict] = None, status: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """ddt_cache_evict. kv pool [rows, row_elems] f32/bf16, score [rows] f32,
+    cache_off [B] i64, cache_len / keep [B] i32. dst None: in place, cache_len
+    advanced to the new lengths; else a dict of kv [dst_rows, row_elems],
+    score [dst_rows], off [B] i64 and layer_stride_rows (several layers): the
+    kept rows go there. max_keep (default: max_cache_len) bounds the kept rows
+    of a request and sizes src; status (optional, [B] i32) receives each
+    request's device status. Returns src [n_layers, B, max_keep] i32 and
+    new_len [B] i32 (in place: cache_len unless given in out)."""
+    _check(kv, "kv", (torch.float32, torch.bfloat16))
+    if kv.dim() != 2:
+        raise ValueError("kv: expected [rows, row_elems]")
+    rows, row_elems = kv.shape
+    B = cache_len.shape[0]
+    _check(score, "score", torch.float32, (rows,))
+    _check(cache_off, "cache_off", torch.int64, (B,))
+    _check(cache_len, "cache_len", torch.int32, (B,))
+    _check(keep, "keep", torch.int32, (B,))
+    d_kv = d_score = d_off = None
+    d_rows = d_stride = 0
+    if dst is not None:
+        d_kv, d_score, d_off = dst["kv"], dst["score"], dst["off"]
+        d_stride = int(dst.get("layer_stride_rows", 0))
+        _check(d_kv, "dst[kv]", kv.dtype)
+        if d_kv.dim() != 2 or d_kv.shape[1] != row_elems:
+            raise ValueError("dst[kv]: expected [rows, row_elems]")
+        d_rows = d_kv.shape[0]
+        _check(d_score, "dst[score]", torch.float32, (d_rows,))
+        _check(d_off, "dst[off]", torch.int64, (B,))
+    if out is None:
+        if max_keep is None:
+            max_keep = max(1, int(max_cache_len))
+        out = {"src": torch.empty(n_layers, B, max_keep, dtype=torch.int32, device=kv.device)}
+    if "new_len" not in out:
+        out["new_len"] = cache_len if dst is None else torch.empty_like(cache_len)
+    if "src" not in out or out["src"].dim() != 3:
+        raise ValueError("out: missing src [n_layers, B, max_keep]")
+    if max_keep is None:
+        max_keep = out["src"].shape[2]
+    _check_out(out, {"src": (torch.int32, (n_layers, B, max_keep)), "new_len": (torch.int32, (B,))})
+    if status is not None:
+        _check(status, "status", torch.int32, (B,))
+    if workspace is None:
+        workspace = torch.empty(cache_evict_workspace_size(B, n_layers, max_cache_len), dtype=torch.uint8, device=kv.device)
+    _check(workspace, "workspace", None)
+    with _device(kv, score, cache_off, cache_len, keep, d_kv, d_score, d_off, status, workspace, *out.values(),
+                 stream=stream):
+        st = load().ddt_cache_evict(_ptr(kv), rows, _dt(kv), row_elems, _ptr(score), n_layers, layer_stride_rows,
+                                    _ptr(cache_off), _ptr(cache_len), _ptr(keep), sink, recent, B,
+                                    int(max_cache_len), _ptr(d_kv), d_rows, _ptr(d_score), d_stride, _ptr(d_off),
+                                    _ptr(out["new_len"]), _ptr(out["src"]), max_keep, _ptr(status),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _raise("ddt_cache_evict", st)
     return out

@@ -441,6 +441,65 @@ DDT_API int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int6
                                const int32_t* tok, int B, int N, int M, int K, float* logp, float* entropy,
                                float* top_logp, int32_t* top_tok, int32_t* dev_status, cudaStream_t stream);
 
+/*
+ * ddt_cache_evict -- hold every request's latent cache to a budget: of the
+ * rows above it, the ones with the least accumulated attention weight go,
+ * and the others close up, in their order, on every layer.
+ *
+ * No counterpart on the pages (their cache only grows by the accept's
+ * compaction). The keys are rotated before they are cached and attention
+ * does not depend on the rows' order, so the remaining rows need no change.
+ *
+ * Definition, per layer l and request b with len = cache_len[b] > keep[b]:
+ *   kept are rows i < sink, rows i >= len - recent, and of the others the
+ *   keep[b] - sink - recent with the largest score (equal scores: the lower
+ *   row first; NaN below every number); each layer chooses by its own scores.
+ *   With src the kept rows in ascending order, row j of the result is row
+ *   src[j], j < keep[b], and its score moves with it. Requests with len <=
+ *   keep[b] keep every row. new_len[b] = min(len, keep[b]).
+ *   kv_dst null: in place (rows from cache_off[b] on; rows and scores behind
+ *   the new length are left as they were, or hold stale copies). Otherwise
+ *   the kept rows and scores go to rows dst_off[b] + j of kv_dst and
+ *   score_dst (every layer l at l * dst_layer_stride_rows more), which must
+ *   not overlap the source rows of any request; the source is unchanged and
+ *   rows of the destination behind the kept ones are not written.
+ *
+ * Inputs (device): kv pool of kv_rows (host value: every layer's rows) rows
+ *   of row_elems elements of kv_dtype (row size a multiple of 4 bytes);
+ *   score [kv_rows] float32, one per pool row (ddt_cache_weights writes
+ *   them); cache_off [B] int64, cache_len [B] int32, keep [B] int32; dst_off
+ *   [B] int64 and kv_dst pool of dst_rows rows with score_dst [dst_rows], or
+ *   all three null (in place). sink, recent >= 0 (host).
+ *   max_cache_len (host): an upper bound on every cache_len[b], of speed only
+ *   (it sizes the selection's shared memory).
+ * Outputs (device): kv / score (in place) or kv_dst / score_dst; new_len [B]
+ *   int32 (may be cache_len itself); src [n_layers][B][max_keep] int32 (-1
+ *   behind the kept rows); dev_status [B] int32 (nullable): DDT_OK;
+ *   DDT_ERR_BOUNDS when rows of the request lie outside a pool (on any
+ *   layer); DDT_ERR_INPUT when keep[b] < 0, or len > keep[b] < sink +
+ *   recent; DDT_ERR_CAPACITY when min(len, keep[b]) > max_keep. Each of these
+ *   skips the request: nothing moves, src is -1, new_len is cache_len[b] in
+ *   place and 0 otherwise.
+ * workspace: ddt_cache_evict_workspace_size(...) bytes, 256-byte
+ *   aligned; its contents do not matter. Calls that share a workspace must
+ *   not overlap in time.
+ * Precondition the library cannot check: the layers and requests own
+ *   disjoint rows.
+ * Two kernels: the selection (one CTA per layer and request) and the copy.
+ *   Neither lets a following kernel start early while it writes the pool.
+ * Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, alignment, only some of
+ *   the destination's pointers, workspace), DDT_ERR_UNSUPPORTED (more than
+ *   2^31 - 1 CTAs), DDT_ERR_CUDA (launch).
+ */
+DDT_API size_t ddt_cache_evict_workspace_size(int B, int n_layers, int max_cache_len);
+
+DDT_API int ddt_cache_evict(void* kv, int64_t kv_rows, int kv_dtype, int row_elems, float* score, int n_layers,
+                            int64_t layer_stride_rows, const int64_t* cache_off, const int32_t* cache_len,
+                            const int32_t* keep, int sink, int recent, int B, int max_cache_len, void* kv_dst,
+                            int64_t dst_rows, float* score_dst, int64_t dst_layer_stride_rows,
+                            const int64_t* dst_off, int32_t* new_len, int32_t* src, int max_keep,
+                            int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
