@@ -93,6 +93,57 @@ int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_
   return ddt::launch_token_logprobs(p, stream);
 }
 
+size_t ddt_cache_weights_workspace_size(int B, int N, int H, int d_qk, int max_cache_len, int in_dtype) {
+  (void)B;
+  (void)N;
+  (void)H;
+  (void)d_qk;
+  (void)max_cache_len;
+  (void)in_dtype;
+  return 0;
+}
+
+int ddt_cache_weights(const void* q, const float* lse, const void* kv, int64_t kv_rows, const int64_t* cache_off,
+                      const int32_t* cache_len, const int32_t* nodes, const int32_t* n_nodes, int B, int N, int M,
+                      int H, int d_qk, float scale, int causal, int max_cache_len, int in_dtype, const float* prev,
+                      float decay, float* score, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+  if (!q || !lse || !kv || !cache_off || !cache_len || !n_nodes || !score) return DDT_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || H < 1 || d_qk < 1 || kv_rows < 1 || max_cache_len < 0 || (nodes && M < 1))
+    return DDT_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !(scale <= 3.402823466e38f) || !(decay - decay == 0.0f)) return DDT_ERR_INVALID_ARG;
+  if (in_dtype != DDT_F32 && in_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
+  const uintptr_t elt = in_dtype == DDT_F32 ? 4 : 2;
+  if (!ddt::aligned(q, elt) || !ddt::aligned(kv, elt)) return DDT_ERR_INVALID_ARG;
+  if (d_qk > 1024 || kv_rows > 0x7fffffffLL || (long long)B * N > 0x7fffffffLL / H ||
+      (nodes && (long long)M * H > 0x7fffffffLL))
+    return DDT_ERR_UNSUPPORTED;
+  ddt::WeightsParams p{};
+  p.q = q;
+  p.lse = lse;
+  p.kv = kv;
+  p.kv_rows = kv_rows;
+  p.cache_off = cache_off;
+  p.cache_len = cache_len;
+  p.nodes = nodes;
+  p.n_nodes = n_nodes;
+  p.B = B;
+  p.N = N;
+  p.M = nodes ? M : N;
+  p.H = H;
+  p.d_qk = d_qk;
+  p.scale = scale;
+  p.causal = causal ? 1 : 0;
+  p.in_dtype = in_dtype;
+  p.prev = prev;
+  p.decay = decay;
+  p.score = score;
+  p.dev_status = dev_status;
+  (void)workspace;
+  (void)workspace_bytes;
+  return ddt::launch_cache_weights_simt(p, max_cache_len, stream);
+}
+
 size_t ddt_cache_evict_workspace_size(int B, int n_layers, int max_cache_len) {
   if (B < 1 || n_layers < 1 || max_cache_len < 0) return 0;
   return ddt::evict_workspace_bytes(B, n_layers, max_cache_len);

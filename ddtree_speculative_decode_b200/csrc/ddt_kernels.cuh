@@ -100,6 +100,28 @@ struct LogprobsParams {
 };
 int launch_token_logprobs(LogprobsParams p, cudaStream_t stream);
 
+// ---- accumulated attention weight of cached rows -----------------------------------
+struct WeightsParams {
+  const void* q;              // [B][N][H][d_qk]
+  const float* lse;           // [B][N][H]
+  const void* kv;             // [kv_rows][d_qk]
+  int64_t kv_rows;
+  const int64_t* cache_off;
+  const int32_t* cache_len;
+  const int32_t* nodes;       // [B][M], nullable: every node below n_nodes
+  const int32_t* n_nodes;
+  int B, N, M, H, d_qk;
+  float scale;
+  int causal;
+  int in_dtype;
+  const float* prev;          // nullable
+  float decay;
+  float* score;               // [kv_rows]
+  int32_t* dev_status;        // [B], nullable
+  int tiles;                  // CUDA-core kernel: key tiles of the launch per request
+};
+int launch_cache_weights_simt(WeightsParams p, int max_cache_len, cudaStream_t stream);
+
 // ---- eviction of cache rows ------------------------------------------------------
 struct EvictParams {
   void* kv;

@@ -35,6 +35,8 @@ EXPORTS = (
     "ddt_accept_compact_lmhead",
     "ddt_drafter_topk",
     "ddt_token_logprobs",
+    "ddt_cache_weights_workspace_size",
+    "ddt_cache_weights",
     "ddt_cache_evict_workspace_size",
     "ddt_cache_evict",
 )
@@ -87,6 +89,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ddt_drafter_topk.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.ddt_token_logprobs.restype = i32
     lib.ddt_token_logprobs.argtypes = [vp, i32, i32, i64, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.ddt_cache_weights_workspace_size.restype = sz
+    lib.ddt_cache_weights_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.ddt_cache_weights.restype = i32
+    lib.ddt_cache_weights.argtypes = [vp, vp, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, i32, vp, f32,
+                                      vp, vp, vp, sz, vp]
     lib.ddt_cache_evict_workspace_size.restype = sz
     lib.ddt_cache_evict_workspace_size.argtypes = [i32, i32, i32]
     lib.ddt_cache_evict.restype = i32
@@ -486,6 +493,63 @@ def token_logprobs(logits: torch.Tensor, tok: torch.Tensor, nodes: Optional[torc
 # ---------------------------------------------------------------------------
 # cache budget
 # ---------------------------------------------------------------------------
+
+
+def cache_weights_workspace_size(B: int, N: int, H: int, d_qk: int, max_cache_len: int, in_dtype: torch.dtype) -> int:
+    """N: the entries per request (nodes.shape[1] with a list)."""
+    return int(load().ddt_cache_weights_workspace_size(B, N, H, d_qk, max_cache_len,
+                                                       DDT_BF16 if in_dtype == torch.bfloat16 else DDT_F32))
+
+
+def cache_weights(q: torch.Tensor, lse: torch.Tensor, kv: torch.Tensor, score: torch.Tensor, cache_off: torch.Tensor,
+                  cache_len: torch.Tensor, n_nodes: torch.Tensor, scale: float, max_cache_len: int,
+                  nodes: Optional[torch.Tensor] = None, causal: bool = False, prev: Optional[torch.Tensor] = None,
+                  decay: float = 1.0, status: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """ddt_cache_weights. q [B, N, H, d_qk] and lse [B, N, H] f32 as given to
+    and by verify_attn, kv pool [rows, d_qk], score [rows] f32 (written in
+    place for the requests' cached rows), cache_off [B] i64, cache_len /
+    n_nodes [B] i32. nodes [B, M] i32 (None: every node): the verify rows that
+    count, up to the first negative entry, e.g. accept_compact's acc_nodes with
+    causal=True. prev [rows] f32: score = decay * prev + weights (pass score
+    itself to accumulate; None: the weights alone). Returns score."""
+    _check(q, "q", (torch.float32, torch.bfloat16))
+    if q.dim() != 4:
+        raise ValueError("q: expected [B, N, H, d_qk]")
+    B, N, H, d = q.shape
+    _check(lse, "lse", torch.float32, (B, N, H))
+    _check(kv, "kv", q.dtype)
+    if kv.dim() != 2 or kv.shape[1] != d:
+        raise ValueError("kv: expected [rows, d_qk]")
+    rows = kv.shape[0]
+    _check(score, "score", torch.float32, (rows,))
+    _check(cache_off, "cache_off", torch.int64, (B,))
+    _check(cache_len, "cache_len", torch.int32, (B,))
+    _check(n_nodes, "n_nodes", torch.int32, (B,))
+    M = 0
+    if nodes is not None:
+        if nodes.dim() != 2:
+            raise ValueError("nodes: expected [B, M]")
+        M = nodes.shape[1]
+        _check(nodes, "nodes", torch.int32, (B, M))
+    if prev is not None:
+        _check(prev, "prev", torch.float32, (rows,))
+    if status is not None:
+        _check(status, "status", torch.int32, (B,))
+    if workspace is None:
+        need = cache_weights_workspace_size(B, M if nodes is not None else N, H, d, max_cache_len, q.dtype)
+        if need > 0:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    else:
+        _check(workspace, "workspace", None)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device(q, lse, kv, score, cache_off, cache_len, n_nodes, nodes, prev, status, workspace, stream=stream):
+        st = load().ddt_cache_weights(_ptr(q), _ptr(lse), _ptr(kv), rows, _ptr(cache_off), _ptr(cache_len),
+                                      _ptr(nodes), _ptr(n_nodes), B, N, M, H, d, float(scale), 1 if causal else 0,
+                                      int(max_cache_len), _dt(q), _ptr(prev), float(decay), _ptr(score),
+                                      _ptr(status), _ptr(workspace), wbytes, _stream(stream))
+    _raise("ddt_cache_weights", st)
+    return score
 
 
 def cache_evict_workspace_size(B: int, n_layers: int, max_cache_len: int) -> int:

@@ -442,6 +442,64 @@ DDT_API int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int6
                                float* top_logp, int32_t* top_tok, int32_t* dev_status, cudaStream_t stream);
 
 /*
+ * ddt_cache_weights -- how much attention every cached row received: the
+ * attention weights of selected verify rows, over all heads, added up per
+ * cached row. The scores that ddt_cache_evict chooses by.
+ *
+ * No counterpart on the pages.
+ *
+ * Definition: with the verify rows' queries q and log-sum-exps lse as given to
+ *   and by ddt_verify_attn, for every cached row j < cache_len[b]
+ *     w_j = sum_e sum_h exp(scale * dot(q[b][i_e][h][:], kv[cache_off[b] + j][:]) - lse[b][i_e][h])
+ *   over the entries e = 0 .. m - 1 whose row sees j, and
+ *     score[cache_off[b] + j] = decay * prev[cache_off[b] + j] + w_j
+ *   (prev null: w_j alone). The entries are i_e = nodes[b][e] up to the first
+ *   negative one (as in acc_nodes; a node listed twice counts twice), or with
+ *   nodes null every node i_e = e < n_nodes[b]. causal 0: every entry sees
+ *   every row j < cache_len[b] (before the accept: the committed cache; its
+ *   tree rows get no weight). causal 1: the entries are the last m of the
+ *   cached rows, entry e sees j < cache_len[b] - m + 1 + e (after the accept:
+ *   nodes = acc_nodes, cache_len advanced; or the end of a prompt).
+ *   A row with lse = -inf (nothing visible) gives no weight; m = 0 leaves
+ *   decay * prev.
+ * Inputs (device): q [B][N][H][d_qk] and kv pool [kv_rows][d_qk] in_dtype;
+ *   lse [B][N][H] float32; cache_off [B] int64, cache_len, n_nodes [B] int32;
+ *   nodes [B][M] int32 (nullable, M unused then); prev [kv_rows] float32
+ *   (nullable; may be score itself). max_cache_len (host): an upper bound on
+ *   every cache_len[b], of speed only (it sizes the launch).
+ * Outputs (device): score [kv_rows] float32, written for the requests' cached
+ *   rows only; dev_status [B] int32 (nullable): DDT_OK; DDT_ERR_BOUNDS when
+ *   the request's rows lie outside the pool; DDT_ERR_INPUT when n_nodes[b] is
+ *   outside [0, N] or a listed node is not below it -- both write nothing for
+ *   the request; DDT_ERR_TIMEOUT when the workspace's status word held a
+ *   timeout (tensor-core kernel).
+ * Supported: in_dtype F32 and BF16, d_qk <= 1024, any H. BF16 with d_qk a
+ *   multiple of 64 up to 576 and 16-byte aligned q and kv runs on the tensor
+ *   cores, the rest on CUDA cores. Dot products and sums are float32, every
+ *   row's sum formed in a fixed order (the same bits on every run).
+ * workspace: at least ddt_cache_weights_workspace_size(...) bytes, 256-byte
+ *   aligned (may be null when that is 0), N there being the entries per
+ *   request (M with a list). Zero it once after allocating; every call that
+ *   returns DDT_OK leaves what must be zero at zero. Its first word is a
+ *   device status: waits inside the tensor-core kernel are bounded
+ *   (ddt_set_wait_limit_ns), and one that expires stores DDT_ERR_TIMEOUT
+ *   there; scores may then be missing, and later calls with that workspace do
+ *   nothing until the caller zeroes it. Calls that share a workspace must not
+ *   overlap in time.
+ * Precondition the library cannot check: the requests own disjoint rows.
+ * Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, scale not finite and
+ *   positive, decay not finite, workspace), DDT_ERR_UNSUPPORTED (d_qk > 1024,
+ *   pools or row counts of 2^31 and more), DDT_ERR_CUDA (launch).
+ */
+DDT_API size_t ddt_cache_weights_workspace_size(int B, int N, int H, int d_qk, int max_cache_len, int in_dtype);
+
+DDT_API int ddt_cache_weights(const void* q, const float* lse, const void* kv, int64_t kv_rows,
+                              const int64_t* cache_off, const int32_t* cache_len, const int32_t* nodes,
+                              const int32_t* n_nodes, int B, int N, int M, int H, int d_qk, float scale, int causal,
+                              int max_cache_len, int in_dtype, const float* prev, float decay, float* score,
+                              int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * ddt_cache_evict -- hold every request's latent cache to a budget: of the
  * rows above it, the ones with the least accumulated attention weight go,
  * and the others close up, in their order, on every layer.
