@@ -94,13 +94,8 @@ int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_
 }
 
 size_t ddt_cache_weights_workspace_size(int B, int N, int H, int d_qk, int max_cache_len, int in_dtype) {
-  (void)B;
-  (void)N;
-  (void)H;
-  (void)d_qk;
-  (void)max_cache_len;
-  (void)in_dtype;
-  return 0;
+  if (B < 1 || N < 1 || H < 1 || max_cache_len < 0) return 0;
+  return ddt::weights_tc_supported(d_qk, in_dtype, nullptr, nullptr) ? ddt::weights_tc_workspace_bytes() : 0;
 }
 
 int ddt_cache_weights(const void* q, const float* lse, const void* kv, int64_t kv_rows, const int64_t* cache_off,
@@ -139,8 +134,12 @@ int ddt_cache_weights(const void* q, const float* lse, const void* kv, int64_t k
   p.decay = decay;
   p.score = score;
   p.dev_status = dev_status;
-  (void)workspace;
-  (void)workspace_bytes;
+  if (ddt::weights_tc_supported(d_qk, in_dtype, nullptr, nullptr)) {
+    if (!workspace || !ddt::aligned(workspace, 256) || workspace_bytes < ddt::weights_tc_workspace_bytes())
+      return DDT_ERR_INVALID_ARG;
+    if (ddt::weights_tc_supported(d_qk, in_dtype, q, kv))
+      return ddt::launch_cache_weights_tc(p, max_cache_len, workspace, stream);
+  }
   return ddt::launch_cache_weights_simt(p, max_cache_len, stream);
 }
 

@@ -122,6 +122,10 @@ struct WeightsParams {
 };
 int launch_cache_weights_simt(WeightsParams p, int max_cache_len, cudaStream_t stream);
 
+bool weights_tc_supported(int d_qk, int in_dtype, const void* q, const void* kv);
+size_t weights_tc_workspace_bytes();
+int launch_cache_weights_tc(WeightsParams p, int max_cache_len, void* workspace, cudaStream_t stream);
+
 // ---- eviction of cache rows ------------------------------------------------------
 struct EvictParams {
   void* kv;
