@@ -273,8 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (aborted) {
     // straight to the teardown
-  } else if (warp == 0 && lane == 0) {
+  } else if (warp == 0) {
     // ============================================================ TMA producer
+    // the whole warp: lane j issues the box of unit j of this CTA's half, whose
+    // row it works out once per tile (one thread issuing every box with its
+    // index arithmetic took 1400 cycles per stage, three times the MMAs' 512)
     const uint32_t afull0 = map_to_rank(bar(kBarAFull), 0), bfull0 = map_to_rank(bar(kBarBFull), 0);
     int slot = 0, issued = 0;
     uint32_t phase = 0, aphase = 0;
@@ -284,33 +287,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && cur.get(s, p, kt, share, nshare, t0, t1); cur.item += npairs) {
       if (t0 >= t1) continue;
       const int b = p.b0 + cur.b, units = s.m[cur.b] * p.chunks;
-      const int y0 = (int)(w.cache_off[b] + kt * 256 + 128 * (int)rank);
+      const int yk = (int)(w.cache_off[b] + kt * 256 + 128 * (int)rank);
       const int32_t* list = w.nodes ? w.nodes + (int64_t)b * w.M : nullptr;
       for (int t = t0; t < t1 && ok; ++t) {
         const Tile tile(p, units, t);
-        const int first = tile.u0 + (leader ? 0 : tile.h0), count = leader ? tile.h0 : tile.nu - tile.h0;
+        const bool mine = lane < (leader ? tile.h0 : tile.nu - tile.h0);
+        int yq = 0;
+        if (mine) {
+          const int u = tile.u0 + (leader ? 0 : tile.h0) + lane, e = u / p.chunks, c = u - e * p.chunks;
+          yq = (b * w.N + (list ? __ldg(list + e) : e)) * w.H + c * p.unit;
+        }
+        const uint32_t dst = sB + (uint32_t)(lane * p.unit * 128);
         for (int k = 0; k < p.slabs; ++k) {
           if (t == t0) {
-            if (!mbar_wait(bar(kBarAEmpty + k), aphase ^ 1u, abort, wlim)) {
-              ok = false;
-              break;
+            if (!mbar_wait(bar(kBarAEmpty + k), aphase ^ 1u, abort, wlim)) ok = false;
+            ok = __all_sync(DDT_FULL_MASK, ok);
+            if (!ok) break;
+            if (lane == 0) {
+              if (leader) mbar_arrive_expect_tx(bar(kBarAFull + k), 2u * kSlabBytes);
+              tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, yk, afull0 + 8u * (uint32_t)k);
             }
-            if (leader) mbar_arrive_expect_tx(bar(kBarAFull + k), 2u * kSlabBytes);
-            tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, y0, afull0 + 8u * (uint32_t)k);
           }
-          if (!mbar_wait(bar(kBarBEmpty + slot), phase ^ 1u, abort, wlim)) {
-            ok = false;
-            break;
-          }
-          if (leader) mbar_arrive_expect_tx(bar(kBarBFull + slot), (uint32_t)(tile.nu * p.unit * 128));
+          if (!mbar_wait(bar(kBarBEmpty + slot), phase ^ 1u, abort, wlim)) ok = false;
+          ok = __all_sync(DDT_FULL_MASK, ok);
+          if (!ok) break;
+          if (leader && lane == 0) mbar_arrive_expect_tx(bar(kBarBFull + slot), (uint32_t)(tile.nu * p.unit * 128));
+          __syncwarp();
           ++issued;
-          const uint32_t dst = sB + (uint32_t)(slot * kSlabBytes);
-          for (int j = 0; j < count; ++j) {
-            const int u = first + j, e = u / p.chunks, c = u - e * p.chunks;
-            const int node = list ? __ldg(list + e) : e;
-            tma_load_2d_pair(dst + (uint32_t)(j * p.unit * 128), &tm_q, 64 * k, (b * w.N + node) * w.H + c * p.unit,
-                             bfull0 + 8u * (uint32_t)slot);
-          }
+          if (mine)
+            tma_load_2d_pair(dst + (uint32_t)(slot * kSlabBytes), &tm_q, 64 * k, yq, bfull0 + 8u * (uint32_t)slot);
           if (++slot == kStages) {
             slot = 0;
             phase ^= 1u;
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       // a wait gave up: let the copies in flight land (bounded) before the
       // CTAs leave; the leader's barriers count both CTAs' bytes
-      if (leader)
+      if (leader && lane == 0)
         for (int i = 0; i < kStages && i < issued; ++i) {
           const int q = issued - 1 - i;
           (void)mbar_wait_own(bar(kBarBFull + q % kStages), (uint32_t)((q / kStages) & 1), abort, wlim);
