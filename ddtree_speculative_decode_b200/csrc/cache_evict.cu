@@ -23,6 +23,7 @@
 // written so far), so no CTA waits for another. Rows before the first
 // evicted one already lie in place and are left alone.
 #include <algorithm>
+#include <mutex>
 
 #include "ddt_kernels.cuh"
 
@@ -244,6 +245,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(EvictParams p
   }
 }
 
+// The selection's shared-memory opt-in, once per device.
+static bool opt_in() {
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev])
+    done[dev] = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) ==
+                cudaSuccess;
+  return done[dev];
+}
+
 template <typename Tv>
 static int launch_move(EvictParams p, cudaStream_t stream) {
   p.row_vecs = p.row_bytes / (int)sizeof(Tv);
@@ -275,9 +289,7 @@ int launch_cache_evict(EvictParams p, int max_cache_len, void* workspace, cudaSt
   // (or one beyond what an SM holds) re-reads its scores instead
   p.held_keys = std::min(kSelKeys, (max_cache_len + 1023) / 1024 * 1024);
   const int smem = p.held_keys * 4;
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) != cudaSuccess)
-    return DDT_ERR_CUDA;
+  if (smem > 32 * 1024 && !opt_in()) return DDT_ERR_CUDA;
   const int st = launch_pdl(evict_select_kernel, (unsigned)(p.n_layers * p.B), kSelThreads, (size_t)smem, stream, p);
   if (st != DDT_OK) return st;
   auto al = [](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
