@@ -73,7 +73,7 @@ int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_
   if (!nodes && M > N) return DDT_ERR_INVALID_ARG;
   if (logits_dtype != DDT_F32 && logits_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
   if (!ddt::aligned(logits, logits_dtype == DDT_F32 ? 4 : 2)) return DDT_ERR_INVALID_ARG;
-  if ((long long)B * M > 0x7fffffffLL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
+  if ((long long)B * M > 0x7fffffffLL || (long long)B * N > 0x7fffffffLL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
   ddt::LogprobsParams p{};
   p.logits = logits;
   p.logits_dtype = logits_dtype;

@@ -10,30 +10,36 @@
 // s e^d and (u + d s) e^d are the sums relative to M.
 //
 // Bound: HBM, every logit of a selected row read once. At 6.5 TB/s an SM gets
-// about 12 bf16 logits per cycle, so a logit may cost about 10 issue slots
-// and 1.3 exponentials' worth of its one ex2 unit per cycle and quarter: the
-// sums run on packed float pairs (about 5 slots per logit) and the top
-// alternatives must cost next to nothing per logit (see below).
+// about 12 bf16 logits per cycle, so a logit may cost 10 issue slots and 1.3
+// turns of the ex2 units: the sums run on packed float pairs relative to an
+// integer power of two (one fma gives a pair's exponents), and that reference
+// moves only when a logit exceeds it by 2^16, so almost never after the first
+// loads.
 //
-// Work split: a fixed grid of 256-thread CTAs (four per SM) in clusters of up
-// to 8; C of them (C | cluster size) share a row, C chosen on the device from
-// the number of selected rows: the C that gives the shortest estimated
-// makespan (rounds of rows x (slice + a fixed cost per slice)). Many rows: C
-// = 1, no exchange at all; few rows: C = 8 for latency. The slices' partial
-// results go to the group's first CTA through distributed shared memory;
-// the cluster barrier they need is split (arrive after a row, wait after the
-// next one), so the join of a row overlaps the next row's loads.
+// Work split: a fixed grid of 256-thread CTAs (three per SM) in clusters of up
+// to 8. Full waves take a row per CTA; the rows left over are shared by C CTAs
+// of a cluster each, C chosen on the device from their number (the shortest
+// estimated makespan: rounds of rows x (slice + a fixed cost per slice)). A
+// slice's result goes to the group's first CTA through distributed shared
+// memory; the cluster barrier for it is split (arrive after a row, wait after
+// the next one), so the join of a row overlaps the next row's loads.
+//
+// Loads: every thread copies its own vectors into its own slots of a
+// three-stage ring in shared memory (cp.async), three rounds of four vectors
+// ahead and across row ends, so the memory stays busy while a row is joined;
+// a thread reads only what it copied, so the ring needs no barrier.
 //
 // Top alternatives: packed keys (order-preserving value bits << 32 | ~index:
-// the larger key is the larger value at the lower index). The first round of
-// loads gives a bound T that at least K keys of the slice reach: each warp
-// sorts its threads' best keys, and T is the r-th largest over the warps of
-// the warp's j-th best (r = min(K, 4), j = ceil(K / r)). From then on a
-// vector costs one compare of its maximum with T's value and a vote; keys
-// that reach T are appended to a buffer in shared memory. A round in which
-// many threads hold such a value (rising rows) raises T from that round's
-// best keys first, which bounds what one round can append. The buffer is
-// sorted into the K best at the end of the slice, or when it runs full.
+// the larger key is the larger value at the lower index). Each warp publishes,
+// after its rounds 0, 2 and 8 and at its end, the j-th largest of its threads'
+// largest values so far; the r-th largest of the warps' is a bound that at
+// least r j >= K values of the slice reach (r = min(K, 4), j = ceil(K / r)),
+// valid however old the published values are, so warps do not wait for one
+// another. A value below the bound costs nothing but its vector's maximum; the
+// others are appended to a buffer in shared memory, cut by the final bound at
+// the end of the slice to few more than K, and sorted by one warp while the
+// others go on. A slice that overruns the buffer (rising rows, rows of few
+// distinct values) is read once more.
 #include <algorithm>
 #include <mutex>
 
@@ -51,15 +57,19 @@ using sm100::smem_u32;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kU = 4;             // 16-byte vectors in flight per thread
+constexpr int kU = 4;             // vectors per thread and round
+constexpr int kRound = kU * kThreads;
+constexpr int kStages = 3;        // rounds of the ring
+constexpr int kRingBytes = kStages * kRound * 16;
 constexpr int kMaxC = 8;          // CTAs that may share a row
-constexpr int kListMax = 4096;    // entries of a launch that follows a node list
-constexpr int kManyThreads = 40;  // more threads than this at T or above: raise T first
-// keys appended between two looks at the buffer's level: a round's from at
-// most kManyThreads threads, or one vector of every thread
-constexpr int kRoundMax = kManyThreads * kU * 8 > kThreads * 8 ? kManyThreads * kU * 8 : kThreads * 8;
-constexpr int kCand = 512 + kRoundMax;
-constexpr float kFar = -150.0f;   // 2^kFar is zero in float32: the floor of the base-2 exponents
+constexpr int kListMax = 1024;    // entries of a launch that follows a node list
+constexpr int kStep = 64;         // threads that add keys between two looks in the careful pass
+constexpr int kCand = 512 + kStep * 8;  // keys of the CTA's buffer
+constexpr int kPick = kCand;      // of these, the ones that reach the final bound
+constexpr float kFar = -150.0f;   // e^kFar and 2^kFar are zero in float32
+constexpr float kUsual = 1e6f;    // below this, a logit in base 2 is off by less than one before it is rounded
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kAhead = 16.0f;   // base-2 exponents may exceed the reference by this much
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -94,6 +104,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 // maximum that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -101,16 +119,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// (m, s, u) of part of a row: m the largest logit (NaN if one is), s and u in
-// base 2: s = sum 2^y, u = sum 2^y y with y = (x - m) log2 e. Empty: m = -inf.
+// (m, s, u) of part of a row: m its largest logit (NaN if one is), s = sum
+// e^d and u = sum e^d d with d = x - m. Empty: m = -inf, s = u = 0.
 struct Sums {
   float m, s, u;
 };
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   const float M = max_nan(a.m, b.m);
-  // an empty part (m = -inf) has s = u = 0: any finite exponent does
-  const float da = fmaxf((a.m - M) * kLog2e, kFar), db = fmaxf((b.m - M) * kLog2e, kFar);
-  const float ea = ex2_ftz(da), eb = ex2_ftz(db);
+  // an empty part has s = u = 0: any finite exponent does
+  const float da = fmaxf(a.m - M, kFar), db = fmaxf(b.m - M, kFar);
+  const float ea = ex2_ftz(da * kLog2e), eb = ex2_ftz(db * kLog2e);
   return {M, a.s * ea + b.s * eb, (a.u + da * a.s) * ea + (b.u + db * b.s) * eb};
 }
 
@@ -132,16 +150,41 @@ __device__ __forceinline__ float value_of(const uint4& r, int t) {
   return __uint_as_float((t & 1) ? (w & 0xffff0000u) : (w << 16));
 }
 
+// two neighbouring values, raised to at least -1e38 (0xfe96 in bf16), where
+// the exponential is zero and the exponent still finite
 template <bool kBF16>
-__device__ __forceinline__ float vec_max(const uint4& r) {  // NaN if one is
+__device__ __forceinline__ void pair_of(const uint4& r, int t, float& a, float& b) {
   if (kBF16) {
-    auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-    const __nv_bfloat162 a = __hmax2_nan(__hmax2_nan(h(r.x), h(r.y)), __hmax2_nan(h(r.z), h(r.w)));
-    return max_nan(__low2float(a), __high2float(a));
+    uint32_t w = t < 2 ? r.x : t < 4 ? r.y : t < 6 ? r.z : r.w;
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xfe96fe96u));
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+  } else {
+    a = fmaxf(value_of<kBF16>(r, t), -1e38f);
+    b = fmaxf(value_of<kBF16>(r, t + 1), -1e38f);
   }
-  return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
-                 max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
 }
+
+// Running maxima of whole vectors, NaN if one is: packed for bf16.
+template <bool kBF16>
+struct Max;
+template <>
+struct Max<true> {
+  __nv_bfloat162 v;
+  __device__ __forceinline__ static __nv_bfloat162 h(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  __device__ __forceinline__ explicit Max(const uint4& r) : v(__hmax2_nan(__hmax2_nan(h(r.x), h(r.y)), __hmax2_nan(h(r.z), h(r.w)))) {}
+  __device__ __forceinline__ void add(const Max& o) { v = __hmax2_nan(v, o.v); }
+  __device__ __forceinline__ float value() const { return max_nan(__low2float(v), __high2float(v)); }
+};
+template <>
+struct Max<false> {
+  float v;
+  __device__ __forceinline__ explicit Max(const uint4& r) {
+    v = max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)), max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+  __device__ __forceinline__ void add(const Max& o) { v = max_nan(v, o.v); }
+  __device__ __forceinline__ float value() const { return v; }
+};
 
 // An end of a row: the elements before full0 (side 0, at the back of the
 // vector) or from full1 on (side 1, at its front); the rest is -inf, which no
@@ -164,16 +207,28 @@ __device__ __noinline__ uint4 load_edge(const unsigned char* row, int V, int ful
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Appends the vector's keys that reach T to the CTA's buffer.
+// Appends the keys of a vector's values that reach T (T's value: tv) to the
+// CTA's buffer. A key that finds the buffer full is lost, but counted.
 template <bool kBF16>
-__device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, unsigned long long* cand, int* count) {
+__device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, float tv, unsigned long long* cand,
+                                         int* count) {
+  unsigned hits = 0u;
 #pragma unroll
-  for (int q = 0; q < Vec<kBF16>::kPer; ++q) {
-    const float x = value_of<kBF16>(v, q);
+  for (int q = 0; q < Vec<kBF16>::kPer; ++q) hits |= value_of<kBF16>(v, q) >= tv ? 1u << q : 0u;
+  while (hits) {
+    const int q = __ffs(hits) - 1;
+    hits &= hits - 1u;
+    float x;
+    if (kBF16) {
+      const uint32_t w = q < 2 ? v.x : q < 4 ? v.y : q < 6 ? v.z : v.w;
+      x = __uint_as_float((q & 1) ? (w & 0xffff0000u) : (w << 16));
+    } else {
+      x = __uint_as_float(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
+    }
     const unsigned long long key = topk_key(x, at + q);
     if (x > -INFINITY && key >= T) {
       const int slot = atomicAdd(count, 1);
-      if (slot < kCand) cand[slot] = key;  // always: see kRoundMax
+      if (slot < kCand) cand[slot] = key;
     }
   }
 }
@@ -184,15 +239,79 @@ __device__ __forceinline__ unsigned long long merge_lists(unsigned long long a, 
   return warp_merge_desc(a > r ? a : r, lane);
 }
 
+// Sorts the buffer's first n keys into its 32 best: every warp its share,
+// then warp 0 the warps' lists. Warp 0 returns the list over its lanes. The
+// caller's barrier comes before; one barrier inside.
+__device__ __forceinline__ unsigned long long best_of(const unsigned long long* cand, int n,
+                                                      unsigned long long (*lists)[32], int warp, int lane) {
+  unsigned long long l = 0ull;
+  for (int c = warp * 32; c < n; c += kThreads) {
+    const int i = c + lane;
+    l = merge_lists(l, warp_sort_desc(i < n ? cand[i] : 0ull, lane), lane);
+  }
+  lists[warp][lane] = l;
+  __syncthreads();
+  if (warp == 0) {
+    const int used = min(kWarps, (n + 31) / 32);
+#pragma unroll 1
+    for (int w = 1; w < used; ++w) l = merge_lists(l, lists[w][lane], lane);
+  }
+  return l;
+}
+
+// The K best keys of a slice whose values defeat the running bound: its whole
+// vectors [v0, v1) once more (and the row's ends, if it has them), kStep
+// threads at a time between looks at the buffer's level, the bound raised to
+// the K-th best key whenever the buffer could run full. Leaves the 32 best.
+template <bool kBF16>
+__device__ __noinline__ void careful_keys(const unsigned char* row, int V, int full0, int full1, int v0, int v1, bool ends,
+                                          int K, unsigned long long* cand, int* count,
+                                          unsigned long long (*lists)[32]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kPer = Vec<kBF16>::kPer;
+  unsigned long long T = 1ull;
+  __syncthreads();
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  for (int r0 = v0; r0 < v1 + (ends ? kStep : 0); r0 += kStep) {
+    const bool end = r0 >= v1;  // the last trip
+    const int i = r0 + tid;
+    const bool mine = end ? tid < 2 : tid < kStep && i < v1;
+    if (mine) {
+      const int pos = end ? (tid == 0 ? full0 - kPer : full1) : full0 + i * kPer;
+      const uint4 x = end ? load_edge<kBF16>(row, V, full0, full1, tid)
+                          : __ldg(reinterpret_cast<const uint4*>(row + (long long)pos * (kBF16 ? 2 : 4)));
+      append_keys<kBF16>(x, pos, T, T == 1ull ? -INFINITY : key_value(T), cand, count);
+    }
+    __syncthreads();
+    if (*count > kCand - kStep * 8) {  // the same for the whole CTA
+      const unsigned long long l = best_of(cand, *count, lists, warp, lane);
+      if (warp == 0) cand[lane] = l;
+      if (tid == 0) *count = 32;
+      __syncthreads();
+      const unsigned long long kth = cand[K - 1];
+      T = kth > T ? kth : T;
+    }
+    if (end) break;
+  }
+  const unsigned long long l = best_of(cand, *count, lists, warp, lane);
+  if (warp == 0) cand[lane] = l;
+  __syncthreads();
+}
+
 template <bool kBF16, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsParams p) {
+__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsParams p) {
+  extern __shared__ __align__(16) unsigned char s_ring[];  // [kStages][kU][kThreads] vectors
   __shared__ uint16_t s_list[kListMax];
-  __shared__ int s_wcount[kWarps], s_live;
+  __shared__ int s_row[kListMax];  // the entry's logits row, -1: no such node
+  __shared__ int s_wcount[kWarps];
   __shared__ Sums s_sums[2][kWarps];
   __shared__ __align__(16) Part s_part[2][kMaxC];
   __shared__ unsigned long long s_cand[kTop ? kCand : 1];
   __shared__ unsigned long long s_lists[kTop ? kWarps : 1][32];
-  __shared__ int s_count;
+  __shared__ unsigned long long s_pick[kTop ? kPick : 1];
+  __shared__ int s_count[2], s_picked;
+  __shared__ uint32_t s_bound[2][kWarps];  // by the row's parity: the warps' j-th largest values, 0 for none
   constexpr int kPer = Vec<kBF16>::kPer;
   constexpr int kElt = kBF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -207,12 +326,12 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
   // not negative; the others are written as skipped by the CTAs in turn
   int live = p.R;
   if (p.nodes) {
-    if (tid == 0) s_live = 0;
-    __syncthreads();
     int base = 0;
     for (int c0 = 0; c0 < p.R; c0 += kThreads) {
       const int e = c0 + tid;
-      const bool on = e < p.R && __ldg(p.nodes + p.e0 + e) >= 0;
+      const long long o = p.e0 + e;
+      const int node = e < p.R ? __ldg(p.nodes + o) : -1;
+      const bool on = node >= 0;
       const unsigned votes = __ballot_sync(DDT_FULL_MASK, on);
       if (lane == 0) s_wcount[warp] = __popc(votes);
       __syncthreads();
@@ -225,9 +344,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
         all += n;
       }
       base += all;
-      if (on) s_list[at] = (uint16_t)e;
+      if (on) {
+        s_list[at] = (uint16_t)e;
+        s_row[at] = node < p.N ? (int)(o / p.M) * p.N + node : -1;
+      }
       if (!on && e < p.R && e % (int)gridDim.x == (int)blockIdx.x) {
-        const long long o = p.e0 + e;
         p.logp[o] = 0.0f;
         if (p.entropy) p.entropy[o] = 0.0f;
         for (int k = 0; k < K; ++k) {
@@ -242,34 +363,115 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
   }
   if (live == 0) return;  // the same on every CTA
 
-  // ---- CTAs per row: the C with the shortest makespan; a slice costs its
-  // vectors plus about kSliceCost vectors' time for its set-up and join
-  constexpr int kSliceCost = 1500;
+  // ---- full waves of a row per CTA, then C CTAs per row for the rows left
+  // over: the C with the shortest makespan; a slice costs its vectors plus
+  // about `fixed` vectors' time for its set-up and join
+  const int grid = (int)gridDim.x;
+  const int waves = live / grid, rest = live - waves * grid;
   int C = 1;
-  {
+  if (rest > 0) {
+    const int fixed = kTop ? 1500 : 500;
     long long best = -1;
     for (int c = 1; c <= csize; c <<= 1) {
-      const long long groups = gridDim.x / c;
-      const long long cost = ((live + groups - 1) / groups) * (V / kPer / c + kSliceCost);
+      const long long groups = grid / c;
+      const long long cost = ((rest + groups - 1) / groups) * (V / kPer / c + fixed);
       if (best < 0 || cost < best) {
         best = cost;
         C = c;
       }
     }
   }
-  const int groups = (int)gridDim.x / C;
+  const int groups = grid / C;
   const int group = (int)blockIdx.x / C, part = (int)blockIdx.x % C;
   const int lead = crank - part;  // the group's first CTA, as a rank of the cluster
-  const int rounds = (live + groups - 1) / groups;
+  const int rows = waves + (rest + groups - 1) / groups;  // of every CTA, some of the last ones empty
   if (C > 1) cluster_sync();      // every CTA of the cluster runs before its shared memory is written
+
+  // the it-th row of this CTA: its entry (-1: none), its logits (null: none)
+  // and its share
+  auto locate = [&](int it, long long& entry, const unsigned char*& row) {
+    const int ord = it < waves ? it * grid + (int)blockIdx.x : waves * grid + (it - waves) * groups + group;
+    entry = -1;
+    row = nullptr;
+    if (it >= rows || ord >= live) return;
+    long long r;
+    if (p.nodes) {
+      entry = p.e0 + s_list[ord];
+      r = s_row[ord];
+    } else {
+      entry = ord;
+      const unsigned b = (unsigned)ord / (unsigned)p.M;
+      r = (long long)b * p.N + ((unsigned)ord - b * (unsigned)p.M);
+    }
+    if (r >= 0) row = static_cast<const unsigned char*>(p.logits) + r * p.row_stride * kElt;
+  };
+  // whole 16-byte vectors of memory in the row: from element full0 on, nfull
+  // of them; what is before and behind are the row's ends
+  auto shape = [&](const unsigned char* row, int& full0, int& nfull) {
+    const int mis = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / kElt);
+    full0 = min(V, mis ? kPer - mis : 0);
+    nfull = (V - full0) / kPer;
+  };
+  auto share = [&](int it, int nfull, int& v0, int& v1) {
+    const int c = it < waves ? 1 : C, k = it < waves ? 0 : part;
+    const int per = (nfull + c - 1) / c;
+    v0 = min(nfull, k * per);
+    v1 = min(nfull, v0 + per);
+  };
+
+  // ---- the copies run ahead of the sums, round by round over all rows
+  const uint32_t ring = smem_u32(s_ring) + (uint32_t)tid * 16u;
+  int f_it = -1, f_left = 0;  // the row being copied and its vectors left, the same for the CTA
+  uint32_t f_slot = 0u;       // byte offset of the stage
+  const unsigned char* f_src = nullptr;
+  auto fetch_round = [&]() {  // of a row with a whole round left
+#pragma unroll
+    for (int u = 0; u < kU; ++u) copy_async(ring + f_slot + (uint32_t)(u * kThreads * 16), f_src + u * kThreads * 16);
+    copy_commit();
+    f_src += kRound * 16;
+    f_left -= kRound;
+    f_slot = f_slot == (kStages - 1) * kRound * 16 ? 0u : f_slot + kRound * 16;
+  };
+  auto fetch = [&]() {
+    while (f_left <= 0 && f_it + 1 < rows) {
+      ++f_it;
+      long long entry;
+      const unsigned char* row;
+      locate(f_it, entry, row);
+      if (row) {
+        int full0, nfull, v0, v1;
+        shape(row, full0, nfull);
+        share(f_it, nfull, v0, v1);
+        f_left = v1 - v0;
+        f_src = row + (long long)full0 * kElt + (long long)(v0 + tid) * 16;
+      }
+    }
+    if (f_left >= kRound) {
+      fetch_round();
+      return;
+    }
+    if (f_left > 0) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (f_left > tid + u * kThreads)
+          copy_async(ring + f_slot + (uint32_t)(u * kThreads * 16), f_src + u * kThreads * 16);
+    }
+    copy_commit();
+    f_src += kRound * 16;
+    f_left -= kRound;
+    f_slot = f_slot == (kStages - 1) * kRound * 16 ? 0u : f_slot + kRound * 16;
+  };
+#pragma unroll 1
+  for (int g = 0; g < kStages; ++g) fetch();
+  uint32_t slot = (uint32_t)tid * 16u;  // of this thread, in the stage the sums are at
 
   // the join of a finished row by warp 0 of the group's first CTA
   float xt = 0.0f, xt_prev = 0.0f;
-  long long ent = -1, ent_prev = -1;
+  long long ent_prev = -1;
   int st = DDT_OK, st_prev = DDT_OK;
-  auto finish = [&](int buf) {
+  auto finish = [&](int buf, int c) {
     const Part* q = s_part[buf];
-    Sums a = lane < C ? q[lane].sums : Sums{-INFINITY, 0.0f, 0.0f};
+    Sums a = lane < c ? q[lane].sums : Sums{-INFINITY, 0.0f, 0.0f};
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
       const Sums b = {__shfl_xor_sync(DDT_FULL_MASK, a.m, o), __shfl_xor_sync(DDT_FULL_MASK, a.s, o),
@@ -281,15 +483,15 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
     a.u = __shfl_sync(DDT_FULL_MASK, a.u, 0);
     // a NaN or +inf logit, or no finite one
     const bool bad = st_prev != DDT_OK || !(fabsf(a.m) <= 3.402823466e38f);
-    const float lns = log2f(a.s) * 0.6931471805599453f;
+    const float lns = log2f(a.s) * kLn2;
     if (lane == 0) {
       p.logp[ent_prev] = bad ? -INFINITY : (xt_prev - a.m) - lns;
-      if (p.entropy) p.entropy[ent_prev] = bad ? 0.0f : fmaxf(lns - 0.6931471805599453f * (a.u / a.s), 0.0f);
+      if (p.entropy) p.entropy[ent_prev] = bad ? 0.0f : fmaxf(lns - a.u / a.s, 0.0f);
       if (p.dev_status) p.dev_status[ent_prev] = bad ? DDT_ERR_INPUT : DDT_OK;
     }
     if (kTop) {
       unsigned long long best = q[0].keys[lane];
-      for (int r = 1; r < C; ++r) best = merge_lists(best, q[r].keys[lane], lane);
+      for (int r = 1; r < c; ++r) best = merge_lists(best, q[r].keys[lane], lane);
       if (lane < K) {
         const bool has = !bad && best != 0ull;
         p.top_logp[ent_prev * K + lane] = has ? (key_value(best) - a.m) - lns : -INFINITY;
@@ -298,163 +500,204 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
     }
   };
 
-  if (kTop && tid == 0) s_count = 0;
-  for (int it = 0; it < rounds; ++it) {
-    const int ord = group + it * groups;
-    const bool on = ord < live;  // the same for the CTAs of a group
+  if (kTop) {
+    if (tid < 2 * kWarps) s_bound[tid / kWarps][tid % kWarps] = 0u;
+    if (tid == 0) s_count[0] = s_count[1] = s_picked = 0;
+    __syncthreads();
+  }
+  for (int it = 0; it < rows; ++it) {
+    const bool whole = it < waves;  // this CTA has the whole row
     const int buf = it & 1;
+    long long ent;
+    const unsigned char* row;
+    locate(it, ent, row);
+    const bool on = ent >= 0;  // the same for the CTAs of a group
     Sums a = {-INFINITY, 0.0f, 0.0f};
-    unsigned long long T = 0ull;  // at least K keys of the slice reach it (0: not known yet)
+    if (kTop) {  // the next row's; nobody uses them before this row's barriers
+      if (lane == 0) s_bound[buf ^ 1][warp] = 0u;
+      if (tid == 0) s_count[buf ^ 1] = 0;
+    }
     if (on) {
-      const int e = p.nodes ? (int)s_list[ord] : ord;
-      const long long o = p.e0 + e;
-      const int b = (int)(o / p.M), j = (int)(o % p.M);
-      const int node = p.nodes ? __ldg(p.nodes + o) : j;
-      const int t = __ldg(p.tok + o);
-      const bool ok = node < p.N && t >= 0 && t < V;
-      ent = o;
-      st = ok ? DDT_OK : DDT_ERR_INPUT;
-      if (node < p.N) {
-        const unsigned char* row =
-            static_cast<const unsigned char*>(p.logits) + ((long long)b * p.N + node) * p.row_stride * kElt;
-        if (part == 0 && warp == 0) {
+      const int t = __ldg(p.tok + ent);
+      st = row && t >= 0 && t < V ? DDT_OK : DDT_ERR_INPUT;
+      if (row) {
+        if ((whole || part == 0) && warp == 0) {
           xt = 0.0f;
-          if (ok) xt = kBF16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + t))
-                             : __ldg(reinterpret_cast<const float*>(row) + t);
+          if (st == DDT_OK) xt = kBF16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + t))
+                                       : __ldg(reinterpret_cast<const float*>(row) + t);
         }
-        // Items of the row: 0 and 1 are its ends, where a 16-byte vector of
-        // memory lies only partly in it (none if aligned); item i >= 2 is the
-        // whole vector at element full0 + (i - 2) kPer.
-        const int mis = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / kElt);
-        const int full0 = min(V, mis ? kPer - mis : 0);
-        const int nfull = (V - full0) / kPer;
+        int full0, nfull, v0, v1;
+        shape(row, full0, nfull);
+        share(it, nfull, v0, v1);
         const int full1 = full0 + nfull * kPer;
-        auto pos_of = [&](int i) { return i >= 2 ? full0 + (i - 2) * kPer : i == 0 ? full0 - kPer : full1; };
-        const int nitem = nfull + 2;
-        const int per = (nitem + C - 1) / C;
-        const int v0 = min(nitem, part * per), v1 = min(nitem, v0 + per);
-        // a vector past the slice counts as all -inf
+        const bool has_ends = (full0 > 0 || full1 < V) && (whole || part == 0);
+        bool ends = has_ends;  // still to come
         const uint32_t inf = kBF16 ? 0xff80ff80u : 0xff800000u;
-        const uint4 none = make_uint4(inf, inf, inf, inf);
-        uint64_t s2 = 0ull, u2 = 0ull;  // packed sums relative to a.m
-        for (int r0 = v0; r0 < v1; r0 += kU * kThreads) {  // the same trips for the whole CTA
-          uint4 v[kU];
-          const unsigned char* src = row + (long long)full0 * kElt + (long long)(r0 + tid - 2) * 16;
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const int i = r0 + tid + u * kThreads;
-            v[u] = none;
-            if (i < v1 && (u > 0 || i >= 2)) v[u] = __ldcs(reinterpret_cast<const uint4*>(src) + u * kThreads);
+        const uint4 none = make_uint4(inf, inf, inf, inf);  // a vector past the slice counts as all -inf
+        // Running sums as packed pairs, s2 = sum 2^y and u2 = sum 2^y y with y
+        // = x log2 e - ref: exact up to one rounding because ref is an integer
+        // (near the thread's largest logit in base 2); limit: the logit that
+        // moves it.
+        uint64_t s2 = 0ull, u2 = 0ull;
+        float ref = 0.0f, limit = -INFINITY;
+        float tv = -INFINITY;  // at least K values of the slice reach it
+        const int first = min(kThreads, max(v1 - v0, ends ? 2 : 0));  // threads with values in round 0
+        const int tr = max(1, min(min(K, 4), (first + 31) / 32)), tj = (K + tr - 1) / tr;
+        // this warp's tj-th largest of its threads' largest values
+        auto publish = [&]() {
+          uint32_t x = a.m > -INFINITY ? float_order_key(a.m) : 0u, top = 0u;
+#pragma unroll 1
+          for (int q = 0; q < tj; ++q) {
+            top = __reduce_max_sync(DDT_FULL_MASK, x);
+            const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
+            if (lane == __ffs(who) - 1) x = 0u;
           }
-          if (r0 + tid < min(2, v1)) v[0] = load_edge<kBF16>(row, V, full0, full1, r0 + tid);
-          float vm[kU];
-          float rm = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            vm[u] = vec_max<kBF16>(v[u]);
-            rm = max_nan(rm, vm[u]);
+          if (lane == 0) *const_cast<volatile uint32_t*>(&s_bound[buf][warp]) = top;
+        };
+        // the tr-th largest of the warps' published values
+        auto bound = [&]() {
+          uint32_t x = lane < kWarps ? *const_cast<volatile uint32_t*>(&s_bound[buf][lane]) : 0u, top = 0u;
+#pragma unroll 1
+          for (int q = 0; q < tr; ++q) {
+            top = __reduce_max_sync(DDT_FULL_MASK, x);
+            const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
+            if (lane == __ffs(who) - 1) x = 0u;
           }
-          if (!(rm <= a.m)) {  // a larger value, or a NaN, which stays
+          if (top != 0u) tv = fmaxf(tv, key_value((unsigned long long)top << 32));
+        };
+        // one round's sums; rm: the largest of its values (NaN if one is)
+        auto sums = [&](const uint4 (&v)[kU], float rm) {
+          if (!(rm <= limit)) {  // far larger than before (or the first), or a NaN, which stays
             const float M = max_nan(rm, a.m);
-            const float d = fmaxf((a.m - M) * kLog2e, kFar), ed = ex2_ftz(d);
-            const uint64_t d2 = pack2(d, d), e2 = pack2(ed, ed);
-            u2 = mul2(fma2(d2, s2, u2), e2);
-            s2 = mul2(s2, e2);
+            float k, e;
+            if (fabsf(a.m) < kUsual) {  // base 2 relative to ref -> base e relative to the old maximum
+              k = fmaf(a.m, -kLog2e, ref);
+              e = ex2_ftz(k);
+              u2 = mul2(fma2(pack2(k, k), s2, u2), pack2(e * kLn2, e * kLn2));
+              s2 = mul2(s2, pack2(e, e));
+            }
+            k = fmaxf(a.m - M, kFar);  // -> relative to the new one (nothing yet: sums of 0)
+            e = ex2_ftz(k * kLog2e);
+            u2 = mul2(fma2(pack2(k, k), s2, u2), pack2(e, e));
+            s2 = mul2(s2, pack2(e, e));
+            limit = M;
+            if (fabsf(M) < kUsual) {  // -> base 2 relative to the new ref
+              ref = ceilf(M * kLog2e);
+              limit = (ref + kAhead) * kLn2;
+              k = fmaf(M, kLog2e, -ref);
+              e = ex2_ftz(k);
+              u2 = mul2(fma2(u2, pack2(kLog2e, kLog2e), mul2(pack2(k, k), s2)), pack2(e, e));
+              s2 = mul2(s2, pack2(e, e));
+            }
             a.m = M;
           }
-          const float nm = a.m == -INFINITY ? 0.0f : -a.m;  // all -inf so far: every term below is 0
-          const uint64_t nm2 = pack2(nm, nm), l2 = pack2(kLog2e, kLog2e);
+          a.m = max_nan(a.m, rm);
+          if (fabsf(a.m) < kUsual) {
+            const uint64_t nr2 = pack2(-ref, -ref), l2 = pack2(kLog2e, kLog2e);
 #pragma unroll
-          for (int u = 0; u < kU; ++u) {
+            for (int u = 0; u < kU; ++u) {
 #pragma unroll
-            for (int q = 0; q < kPer; q += 2) {
-              const uint64_t y = mul2(add2(pack2(value_of<kBF16>(v[u], q), value_of<kBF16>(v[u], q + 1)), nm2), l2);
-              float y0, y1;
-              unpack2(y, y0, y1);
-              y0 = fmaxf(y0, kFar);
-              y1 = fmaxf(y1, kFar);
-              const uint64_t e = pack2(ex2_ftz(y0), ex2_ftz(y1));
-              s2 = add2(s2, e);
-              u2 = fma2(e, pack2(y0, y1), u2);
+              for (int q = 0; q < kPer; q += 2) {
+                float x0, x1, y0, y1;
+                pair_of<kBF16>(v[u], q, x0, x1);
+                const uint64_t y = fma2(pack2(x0, x1), l2, nr2);
+                unpack2(y, y0, y1);
+                const uint64_t e = pack2(ex2_ftz(y0), ex2_ftz(y1));
+                s2 = add2(s2, e);
+                u2 = fma2(e, y, u2);
+              }
+            }
+          } else if (a.m != -INFINITY) {
+            // rows of extreme values: s2 and u2 are sums of e^d and e^d d, d =
+            // x - m, cut where the exponential is zero
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+#pragma unroll
+              for (int q = 0; q < kPer; ++q) {
+                const float d = fmaxf(value_of<kBF16>(v[u], q) - a.m, kFar), e = ex2_ftz(d * kLog2e);
+                s2 = add2(s2, pack2(e, 0.0f));
+                u2 = fma2(pack2(e, 0.0f), pack2(d, 0.0f), u2);
+              }
             }
           }
-          if (kTop) {
-            // raise T from this round's best keys: in the first round, or when
-            // so many threads hold a value at T that they could fill the buffer
-            auto reaches = [&](float x) { return x > -INFINITY && (T == 0ull || x >= key_value(T)); };
-            const bool first = r0 == v0;
-            int holders = __syncthreads_count(reaches(rm));
-            if (first || holders > kManyThreads) {
-              unsigned long long best = 0ull;
-              if (rm > -INFINITY) {  // the lowest index of this thread's largest value
-                int at = 0;
+        };
+        // one round's alternatives; at: element of this thread's first value
+        auto top = [&](const uint4 (&v)[kU], float rm, int r, int at) {
+          if (r == 0 || r == 2 || r == 8) {
+            publish();
+            if (r == 0) __syncthreads();  // a first bound needs every warp's
+            bound();
+          } else if ((r & 3) == 0) {
+            bound();
+          }
+          if (rm >= tv && rm > -INFINITY) {
 #pragma unroll
-                for (int u = kU - 1; u >= 0; --u) {
-                  if (vm[u] == rm) {
-                    int k = kPer;
+            for (int u = 0; u < kU; ++u)
+              append_keys<kBF16>(v[u], at + u * kThreads * kPer, 0ull, tv, s_cand, &s_count[buf]);
+          }
+        };
+        auto largest = [&](const uint4 (&v)[kU]) {
+          Max<kBF16> m(v[0]);
 #pragma unroll
-                    for (int q = kPer - 1; q >= 0; --q)
-                      if (value_of<kBF16>(v[u], q) == rm) k = q;
-                    at = pos_of(r0 + tid + u * kThreads) + k;
-                  }
-                }
-                best = topk_key(rm, at);
-              }
-              best = warp_sort_desc(best, lane);
-              s_lists[warp][lane] = best;
-              __syncthreads();
-              const int r = min(K, 4), jj = (K + r - 1) / r - 1;
-              const unsigned long long c = lane < kWarps ? s_lists[lane][jj] : 0ull;
-              int above = 0;  // warps whose j-th best is larger (equal: the lower warp first)
-#pragma unroll
-              for (int w = 0; w < kWarps; ++w) {
-                const unsigned long long d = __shfl_sync(DDT_FULL_MASK, c, w);
-                above += (d > c || (d == c && w < lane)) ? 1 : 0;
-              }
-              const unsigned pick = __ballot_sync(DDT_FULL_MASK, lane < kWarps && above == r - 1);
-              const unsigned long long cand = __shfl_sync(DDT_FULL_MASK, c, __ffs(pick) - 1);
-              T = cand > T ? cand : T;
-              holders = __syncthreads_count(reaches(rm));
-            }
-            // still many (rows of few distinct values): look at the buffer's
-            // level after every vector instead of after the round
-            const bool many = holders > kManyThreads;
-            if (!many) {
-#pragma unroll
-              for (int u = 0; u < kU; ++u)
-                if (reaches(vm[u])) append_keys<kBF16>(v[u], pos_of(r0 + tid + u * kThreads), T, s_cand, &s_count);
-            }
+          for (int u = 1; u < kU; ++u) m.add(Max<kBF16>(v[u]));
+          return m.value();
+        };
+        auto next_slot = [&](uint32_t x) { return x >= (kStages - 1) * kRound * 16 ? x - (kStages - 1) * kRound * 16 : x + kRound * 16; };
+        int left = v1 - v0, r = 0, at = full0 + (v0 + tid) * kPer;
+        // whole rounds with whole rounds to copy behind them: no conditions
+        // but the rare ones
 #pragma unroll 1
-            for (int u = many ? 0 : kU - 1; u < kU; ++u) {
-              if (many) {
-                const int i = r0 + tid + u * kThreads;  // read again: a register array cannot be indexed by u
-                if (i < v1) {
-                  const uint4 x = i < 2 ? load_edge<kBF16>(row, V, full0, full1, i)
-                                        : __ldg(reinterpret_cast<const uint4*>(src) + u * kThreads);
-                  if (reaches(vec_max<kBF16>(x))) append_keys<kBF16>(x, pos_of(i), T, s_cand, &s_count);
-                }
-              }
-              __syncthreads();
-              if (s_count > kCand - kRoundMax) {  // the same for the whole CTA
-                // sort the buffer into its 32 best, which stay as its first entries
-                const int n = min(s_count, kCand);
-                unsigned long long l = 0ull;
-                for (int c = warp * 32; c < n; c += kThreads) {
-                  const int i = c + lane;
-                  l = merge_lists(l, warp_sort_desc(i < n ? s_cand[i] : 0ull, lane), lane);
-                }
-                s_lists[warp][lane] = l;
-                __syncthreads();
-                if (warp == 0) {
+        for (; left >= kRound && f_left >= kRound; left -= kRound, ++r, at += kRound * kPer) {
+          uint4 v[kU];
+          copy_wait<kStages - 1>();
+          const unsigned char* from = s_ring + slot;
+#pragma unroll
+          for (int u = 0; u < kU; ++u) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
+          slot = next_slot(slot);
+          const float rm = largest(v);
+          fetch_round();  // this round's vectors are in registers: their slots are free
+          sums(v, rm);
+          if (kTop) top(v, rm, r, at);
+        }
 #pragma unroll 1
-                  for (int w = 1; w < kWarps; ++w) l = merge_lists(l, s_lists[w][lane], lane);
-                  s_cand[lane] = l;
-                  if (lane == 0) s_count = 32;
-                }
-                __syncthreads();
-                const unsigned long long kth = s_cand[K - 1];
-                T = kth > T ? kth : T;
-              }
+        for (; left > 0 || ends; left -= kRound, ++r, at += kRound * kPer) {
+          uint4 v[kU];
+#pragma unroll
+          for (int u = 0; u < kU; ++u) v[u] = none;
+          int pos = at;
+          if (left > 0) {
+            copy_wait<kStages - 1>();
+            const unsigned char* from = s_ring + slot;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+              if (left > tid + u * kThreads) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
+            slot = next_slot(slot);
+          } else {  // the row's ends
+            ends = false;
+            if (tid < 2) v[0] = load_edge<kBF16>(row, V, full0, full1, tid);
+            pos = tid == 0 ? full0 - kPer : full1;
+          }
+          const float rm = largest(v);
+          if (left > 0) fetch();
+          sums(v, rm);
+          if (kTop) top(v, rm, r, pos);
+        }
+        if (kTop) {
+          // of the buffer, the keys that reach the final bound: few more than K
+          if (r > 0) publish();
+          __syncthreads();
+          bound();
+          int n = s_count[buf];
+          if (n > kCand) {  // keys were lost: the same for the whole CTA
+            careful_keys<kBF16>(row, V, full0, full1, v0, v1, has_ends, K, s_cand, &s_count[buf], s_lists);
+            n = 32;
+            tv = -INFINITY;
+          }
+          for (int i = tid; i < n; i += kThreads) {
+            const unsigned long long key = s_cand[i];
+            if (key != 0ull && key_value(key) >= tv) {
+              const int at = atomicAdd(&s_picked, 1);
+              if (at < kPick) s_pick[at] = key;
             }
           }
         }
@@ -463,6 +706,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
         unpack2(u2, u0, u1);
         a.s = s0 + s1;
         a.u = u0 + u1;
+        if (fabsf(a.m) < kUsual) {  // from base 2 relative to ref to base e relative to m
+          const float k = fmaf(a.m, -kLog2e, ref), ek = ex2_ftz(k);  // -kAhead <= k <= 1
+          a.u = (a.u + k * a.s) * ek * kLn2;
+          a.s *= ek;
+        }
       }
 #pragma unroll
       for (int q = 16; q > 0; q >>= 1) {
@@ -473,27 +721,22 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
       if (lane == 0) s_sums[buf][warp] = a;
     }
     __syncthreads();
-    unsigned long long l = 0ull;
-    if (kTop) {
-      const int n = min(s_count, kCand);
-      for (int c = warp * 32; c < n; c += kThreads) {
-        const int i = c + lane;
-        l = merge_lists(l, warp_sort_desc(i < n ? s_cand[i] : 0ull, lane), lane);
-      }
-      s_lists[warp][lane] = l;
-      __syncthreads();
-      if (tid == 0) s_count = 0;
-      if (warp == 0) {
-        const int lists = min(kWarps, (n + 31) / 32);
+    unsigned long long l = 0ull;  // warp 0: the slice's best keys over the lanes
+    if (kTop && warp == 0) {
+      const int n = s_picked;
 #pragma unroll 1
-        for (int w = 1; w < lists; ++w) l = merge_lists(l, s_lists[w][lane], lane);
+      for (int c = 0; c < n; c += 32) {
+        const unsigned long long x = warp_sort_desc(c + lane < n ? s_pick[c + lane] : 0ull, lane);
+        l = c == 0 ? x : merge_lists(l, x, lane);
       }
+      __syncwarp();
+      if (lane == 0) s_picked = 0;
     }
-    // the row before this one is complete in the group's first CTA
+    // the shared row before this one is complete in the group's first CTA
     __syncwarp();
-    if (C > 1 && it > 0) {
+    if (C > 1 && it > waves) {
       cluster_wait();
-      if (part == 0 && warp == 0 && ent_prev >= 0) finish(buf ^ 1);
+      if (part == 0 && warp == 0 && ent_prev >= 0) finish(buf ^ 1, C);
     }
     if (warp == 0 && on) {
       Sums b = lane < kWarps ? s_sums[buf][lane] : Sums{-INFINITY, 0.0f, 0.0f};
@@ -503,8 +746,9 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
                         __shfl_xor_sync(DDT_FULL_MASK, b.u, q)};
         b = join(b, c);
       }
-      Part* dst = &s_part[buf][part];
-      if (C > 1 && part != 0) {
+      const int to = whole ? 0 : part;
+      Part* dst = &s_part[buf][to];
+      if (to != 0) {
         const uint32_t base = map_to_rank(smem_u32(dst), (uint32_t)lead);
         if (lane == 0) {
           st_cluster_f32(base, b.m);
@@ -522,15 +766,17 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobsPar
     ent_prev = on ? ent : -1;
     st_prev = st;
     xt_prev = xt;
-    if (C > 1) {
+    if (!whole && C > 1) {
       cluster_arrive();
     } else if (warp == 0 && on) {
-      finish(buf);
+      finish(buf, 1);
+      __syncwarp();
     }
   }
+  copy_wait<0>();
   if (C > 1) {
     cluster_wait();
-    if (part == 0 && warp == 0 && ent_prev >= 0) finish((rounds - 1) & 1);
+    if (part == 0 && warp == 0 && ent_prev >= 0) finish((rows - 1) & 1, C);
   }
 }
 
@@ -539,7 +785,7 @@ static cudaLaunchConfig_t config(cudaLaunchAttribute* attr, int grid, int cluste
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -552,38 +798,49 @@ static cudaLaunchConfig_t config(cudaLaunchAttribute* attr, int grid, int cluste
   return cfg;
 }
 
-// CTAs of the kernel resident at once in clusters of 8 on the current device
-// (0: such clusters cannot be scheduled), looked up once per device.
+// CTAs of the kernel resident at once in such clusters on the current device
+// (0: such clusters cannot be scheduled; -1: no such device), looked up once per
+// device (with the shared-memory opt-in set).
 template <bool kBF16, bool kTop>
-static int resident_ctas() {
+static int resident_ctas(int cluster) {
   static std::mutex mu;
-  static int known[kMaxDevices];
-  static bool have[kMaxDevices] = {false};
+  static int known[kMaxDevices][kMaxC + 1];
+  static bool have[kMaxDevices][kMaxC + 1] = {};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
   std::lock_guard<std::mutex> lock(mu);
-  if (!have[dev]) {
+  if (!have[dev][cluster]) {
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config<kBF16, kTop>(attr, 4096, kMaxC, nullptr);
+    cudaLaunchConfig_t cfg = config<kBF16, kTop>(attr, 4096, cluster, nullptr);
+    if (cudaFuncSetAttribute(token_logprobs_kernel<kBF16, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRingBytes) != cudaSuccess)
+      return -1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, token_logprobs_kernel<kBF16, kTop>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       n = 0;
     }
-    known[dev] = n * kMaxC;
-    have[dev] = true;
+    known[dev][cluster] = n * cluster;
+    have[dev][cluster] = true;
   }
-  return known[dev];
+  return known[dev][cluster];
 }
 
 template <bool kBF16, bool kTop>
 static int launch_t(LogprobsParams p, cudaStream_t stream) {
   // slices of at least 4 KB; no more CTAs than the rows can use
   const int elt = kBF16 ? 2 : 4;
-  const int slots = resident_ctas<kBF16, kTop>();
-  int cluster = kMaxC;
-  while (cluster > 1 && (slots == 0 || (long long)p.V * elt < 4096LL * cluster)) cluster >>= 1;
-  const long long most = std::max(1, (slots > 0 ? slots : 4 * sm_count()) / cluster);
+  // a row shared by many CTAs for latency while the rows are few (or may be: a
+  // node list usually selects a path); smaller clusters leave fewer SMs unused
+  int cluster = p.nodes || (long long)p.B * p.M * kMaxC <= sm_count() * 3 ? kMaxC : 4;
+  while (cluster > 1 && (long long)p.V * elt < 4096LL * cluster) cluster >>= 1;
+  int slots = 0;
+  for (;; cluster >>= 1) {
+    slots = resident_ctas<kBF16, kTop>(cluster);
+    if (slots < 0) return DDT_ERR_CUDA;
+    if (slots > 0 || cluster == 1) break;
+  }
+  const long long most = std::max(1, (slots > 0 ? slots : 3 * sm_count()) / cluster);
   p.cluster = cluster;
   const long long total = (long long)p.B * p.M;
   const long long step = p.nodes ? kListMax : total;
