@@ -97,6 +97,7 @@ struct LogprobsParams {
   int64_t e0;             // first entry of this launch
   int R;                  // entries of this launch
   int cluster;            // CTAs per cluster
+  int log_share;          // log2 of the CTAs that share a row; -1: decided on the device
 };
 int launch_token_logprobs(LogprobsParams p, cudaStream_t stream);
 

@@ -64,7 +64,7 @@ constexpr int kRingBytes = kStages * kRound * 16;
 constexpr int kMaxC = 8;          // CTAs that may share a row
 constexpr int kListMax = 1024;    // entries of a launch that follows a node list
 constexpr int kStep = 64;         // threads that add keys between two looks in the careful pass
-constexpr int kCand = 512 + kStep * 8;  // keys of the CTA's buffer
+constexpr int kCand = 256 + kStep * 8;  // keys of the CTA's buffer
 constexpr int kPick = kCand;      // of these, the ones that reach the final bound
 constexpr float kFar = -150.0f;   // e^kFar and 2^kFar are zero in float32
 constexpr float kUsual = 1e6f;    // below this, a logit in base 2 is off by less than one before it is rounded
@@ -124,12 +124,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 struct Sums {
   float m, s, u;
 };
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
-  const float M = max_nan(a.m, b.m);
-  // an empty part has s = u = 0: any finite exponent does
-  const float da = fmaxf(a.m - M, kFar), db = fmaxf(b.m - M, kFar);
-  const float ea = ex2_ftz(da * kLog2e), eb = ex2_ftz(db * kLog2e);
-  return {M, a.s * ea + b.s * eb, (a.u + da * a.s) * ea + (b.u + db * b.s) * eb};
+// The join of kLanes lanes' parts (a power of two), in every one of them: their
+// largest m, and the sums relative to it.
+template <int kLanes>
+__device__ __forceinline__ Sums join(Sums a) {
+  float M = a.m;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(DDT_FULL_MASK, M, o));
+  const float d = fmaxf(a.m - M, kFar), e = ex2_ftz(d * kLog2e);  // an empty part has s = u = 0: any finite d does
+  a.u = (a.u + d * a.s) * e;
+  a.s *= e;
+  a.m = M;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(DDT_FULL_MASK, a.s, o);
+    a.u += __shfl_xor_sync(DDT_FULL_MASK, a.u, o);
+  }
+  return a;
 }
 
 struct Part {  // one CTA's share of a row
@@ -233,10 +244,30 @@ __device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, 
   }
 }
 
+// One key per lane into descending order; rolled and out of line, as is the
+// merge: both run once or a few times per row, and a row's latency is mostly
+// the code that has to be fetched for it.
+__device__ __noinline__ unsigned long long sort_list(unsigned long long x, int lane) {
+#pragma unroll 1
+  for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll 1
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const unsigned long long y = __shfl_xor_sync(DDT_FULL_MASK, x, j);
+      x = (((lane & j) == 0) == ((lane & k) == 0)) == (y > x) ? y : x;
+    }
+  }
+  return x;
+}
 // merge of two lists sorted over the lanes (descending): the 32 best, sorted
-__device__ __forceinline__ unsigned long long merge_lists(unsigned long long a, unsigned long long b, int lane) {
+__device__ __noinline__ unsigned long long merge_lists(unsigned long long a, unsigned long long b, int lane) {
   const unsigned long long r = __shfl_sync(DDT_FULL_MASK, b, 31 - lane);
-  return warp_merge_desc(a > r ? a : r, lane);
+  unsigned long long x = a > r ? a : r;
+#pragma unroll 1
+  for (int j = 16; j > 0; j >>= 1) {
+    const unsigned long long y = __shfl_xor_sync(DDT_FULL_MASK, x, j);
+    x = ((lane & j) == 0) == (y > x) ? y : x;
+  }
+  return x;
 }
 
 // Sorts the buffer's first n keys into its 32 best: every warp its share,
@@ -247,7 +278,7 @@ __device__ __forceinline__ unsigned long long best_of(const unsigned long long* 
   unsigned long long l = 0ull;
   for (int c = warp * 32; c < n; c += kThreads) {
     const int i = c + lane;
-    l = merge_lists(l, warp_sort_desc(i < n ? cand[i] : 0ull, lane), lane);
+    l = merge_lists(l, sort_list(i < n ? cand[i] : 0ull, lane), lane);
   }
   lists[warp][lane] = l;
   __syncthreads();
@@ -368,21 +399,23 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   // about `fixed` vectors' time for its set-up and join
   const int grid = (int)gridDim.x;
   const int waves = live / grid, rest = live - waves * grid;
-  int C = 1;
-  if (rest > 0) {
+  int lc = p.log_share;  // log2 of C
+  if (lc < 0) {
+    lc = 0;
     const int fixed = kTop ? 1500 : 500;
     long long best = -1;
-    for (int c = 1; c <= csize; c <<= 1) {
-      const long long groups = grid / c;
-      const long long cost = ((rest + groups - 1) / groups) * (V / kPer / c + fixed);
+    for (int l = 0; rest > 0 && (1 << l) <= csize; ++l) {
+      const int g = grid >> l;
+      const long long cost = (long long)((rest + g - 1) / g) * ((V / kPer >> l) + fixed);
       if (best < 0 || cost < best) {
         best = cost;
-        C = c;
+        lc = l;
       }
     }
   }
-  const int groups = grid / C;
-  const int group = (int)blockIdx.x / C, part = (int)blockIdx.x % C;
+  const int C = 1 << lc;
+  const int groups = grid >> lc;
+  const int group = (int)blockIdx.x >> lc, part = (int)blockIdx.x & (C - 1);
   const int lead = crank - part;  // the group's first CTA, as a rank of the cluster
   const int rows = waves + (rest + groups - 1) / groups;  // of every CTA, some of the last ones empty
   if (C > 1) cluster_sync();      // every CTA of the cluster runs before its shared memory is written
@@ -413,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     nfull = (V - full0) / kPer;
   };
   auto share = [&](int it, int nfull, int& v0, int& v1) {
-    const int c = it < waves ? 1 : C, k = it < waves ? 0 : part;
-    const int per = (nfull + c - 1) / c;
+    const int l = it < waves ? 0 : lc, k = it < waves ? 0 : part;
+    const int per = (nfull + (1 << l) - 1) >> l;
     v0 = min(nfull, k * per);
     v1 = min(nfull, v0 + per);
   };
@@ -469,33 +502,29 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   float xt = 0.0f, xt_prev = 0.0f;
   long long ent_prev = -1;
   int st = DDT_OK, st_prev = DDT_OK;
-  auto finish = [&](int buf, int c) {
+  auto finish = [&](int buf, int c, long long entry, float x, int status) {
     const Part* q = s_part[buf];
     Sums a = lane < c ? q[lane].sums : Sums{-INFINITY, 0.0f, 0.0f};
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
-      const Sums b = {__shfl_xor_sync(DDT_FULL_MASK, a.m, o), __shfl_xor_sync(DDT_FULL_MASK, a.s, o),
-                      __shfl_xor_sync(DDT_FULL_MASK, a.u, o)};
-      a = join(a, b);
-    }
+    a = join<kMaxC>(a);
     a.m = __shfl_sync(DDT_FULL_MASK, a.m, 0);
     a.s = __shfl_sync(DDT_FULL_MASK, a.s, 0);
     a.u = __shfl_sync(DDT_FULL_MASK, a.u, 0);
     // a NaN or +inf logit, or no finite one
-    const bool bad = st_prev != DDT_OK || !(fabsf(a.m) <= 3.402823466e38f);
+    const bool bad = status != DDT_OK || !(fabsf(a.m) <= 3.402823466e38f);
     const float lns = log2f(a.s) * kLn2;
     if (lane == 0) {
-      p.logp[ent_prev] = bad ? -INFINITY : (xt_prev - a.m) - lns;
-      if (p.entropy) p.entropy[ent_prev] = bad ? 0.0f : fmaxf(lns - a.u / a.s, 0.0f);
-      if (p.dev_status) p.dev_status[ent_prev] = bad ? DDT_ERR_INPUT : DDT_OK;
+      p.logp[entry] = bad ? -INFINITY : (x - a.m) - lns;
+      if (p.entropy) p.entropy[entry] = bad ? 0.0f : fmaxf(lns - a.u / a.s, 0.0f);
+      if (p.dev_status) p.dev_status[entry] = bad ? DDT_ERR_INPUT : DDT_OK;
     }
     if (kTop) {
       unsigned long long best = q[0].keys[lane];
+#pragma unroll 1
       for (int r = 1; r < c; ++r) best = merge_lists(best, q[r].keys[lane], lane);
       if (lane < K) {
         const bool has = !bad && best != 0ull;
-        p.top_logp[ent_prev * K + lane] = has ? (key_value(best) - a.m) - lns : -INFINITY;
-        p.top_tok[ent_prev * K + lane] = has ? static_cast<int32_t>(~static_cast<uint32_t>(best)) : -1;
+        p.top_logp[entry * K + lane] = has ? (key_value(best) - a.m) - lns : -INFINITY;
+        p.top_tok[entry * K + lane] = has ? static_cast<int32_t>(~static_cast<uint32_t>(best)) : -1;
       }
     }
   };
@@ -505,8 +534,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     if (tid == 0) s_count[0] = s_count[1] = s_picked = 0;
     __syncthreads();
   }
-  for (int it = 0; it < rows; ++it) {
-    const bool whole = it < waves;  // this CTA has the whole row
+#pragma unroll 1
+  for (int it = 0; it < rows + (C > 1 ? 1 : 0); ++it) {  // shared rows are joined a turn later
+    const bool whole = it < waves || C == 1;  // this CTA has the whole row
     const int buf = it & 1;
     long long ent;
     const unsigned char* row;
@@ -542,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         float ref = 0.0f, limit = -INFINITY;
         float tv = -INFINITY;  // at least K values of the slice reach it
         const int first = min(kThreads, max(v1 - v0, ends ? 2 : 0));  // threads with values in round 0
-        const int tr = max(1, min(min(K, 4), (first + 31) / 32)), tj = (K + tr - 1) / tr;
+        const int tr = max(1, min(min(K, 4), (first + 31) / 32)), tj = tr == 1 ? K : tr == 2 ? (K + 1) >> 1 : tr == 4 ? (K + 3) >> 2 : (K + 2) / 3;
         // this warp's tj-th largest of its threads' largest values
         auto publish = [&]() {
           uint32_t x = a.m > -INFINITY ? float_order_key(a.m) : 0u, top = 0u;
@@ -627,13 +657,14 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
             publish();
             if (r == 0) __syncthreads();  // a first bound needs every warp's
             bound();
-          } else if ((r & 3) == 0) {
+          } else if (r == 1 || (r & 3) == 0) {
             bound();
           }
           if (rm >= tv && rm > -INFINITY) {
 #pragma unroll
             for (int u = 0; u < kU; ++u)
-              append_keys<kBF16>(v[u], at + u * kThreads * kPer, 0ull, tv, s_cand, &s_count[buf]);
+              if (Max<kBF16>(v[u]).value() >= tv)
+                append_keys<kBF16>(v[u], at + u * kThreads * kPer, 0ull, tv, s_cand, &s_count[buf]);
           }
         };
         auto largest = [&](const uint4 (&v)[kU]) {
@@ -644,10 +675,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         };
         auto next_slot = [&](uint32_t x) { return x >= (kStages - 1) * kRound * 16 ? x - (kStages - 1) * kRound * 16 : x + kRound * 16; };
         int left = v1 - v0, r = 0, at = full0 + (v0 + tid) * kPer;
-        // whole rounds with whole rounds to copy behind them: no conditions
-        // but the rare ones
+        // whole rounds: no conditions but the rare ones
 #pragma unroll 1
-        for (; left >= kRound && f_left >= kRound; left -= kRound, ++r, at += kRound * kPer) {
+        for (; left >= kRound; left -= kRound, ++r, at += kRound * kPer) {
           uint4 v[kU];
           copy_wait<kStages - 1>();
           const unsigned char* from = s_ring + slot;
@@ -655,7 +685,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
           for (int u = 0; u < kU; ++u) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
           slot = next_slot(slot);
           const float rm = largest(v);
-          fetch_round();  // this round's vectors are in registers: their slots are free
+          // this round's vectors are in registers: their slots are free
+          if (f_left >= kRound) fetch_round();
+          else fetch();
           sums(v, rm);
           if (kTop) top(v, rm, r, at);
         }
@@ -712,12 +744,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
           a.s *= ek;
         }
       }
-#pragma unroll
-      for (int q = 16; q > 0; q >>= 1) {
-        const Sums c = {__shfl_xor_sync(DDT_FULL_MASK, a.m, q), __shfl_xor_sync(DDT_FULL_MASK, a.s, q),
-                        __shfl_xor_sync(DDT_FULL_MASK, a.u, q)};
-        a = join(a, c);
-      }
+      a = join<32>(a);
       if (lane == 0) s_sums[buf][warp] = a;
     }
     __syncthreads();
@@ -726,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       const int n = s_picked;
 #pragma unroll 1
       for (int c = 0; c < n; c += 32) {
-        const unsigned long long x = warp_sort_desc(c + lane < n ? s_pick[c + lane] : 0ull, lane);
+        const unsigned long long x = sort_list(c + lane < n ? s_pick[c + lane] : 0ull, lane);
         l = c == 0 ? x : merge_lists(l, x, lane);
       }
       __syncwarp();
@@ -734,18 +761,10 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     }
     // the shared row before this one is complete in the group's first CTA
     __syncwarp();
-    if (C > 1 && it > waves) {
-      cluster_wait();
-      if (part == 0 && warp == 0 && ent_prev >= 0) finish(buf ^ 1, C);
-    }
+    const bool turn = C > 1 && it > waves;
+    if (turn) cluster_wait();
     if (warp == 0 && on) {
-      Sums b = lane < kWarps ? s_sums[buf][lane] : Sums{-INFINITY, 0.0f, 0.0f};
-#pragma unroll
-      for (int q = 4; q > 0; q >>= 1) {
-        const Sums c = {__shfl_xor_sync(DDT_FULL_MASK, b.m, q), __shfl_xor_sync(DDT_FULL_MASK, b.s, q),
-                        __shfl_xor_sync(DDT_FULL_MASK, b.u, q)};
-        b = join(b, c);
-      }
+      const Sums b = join<kWarps>(lane < kWarps ? s_sums[buf][lane] : Sums{-INFINITY, 0.0f, 0.0f});
       const int to = whole ? 0 : part;
       Part* dst = &s_part[buf][to];
       if (to != 0) {
@@ -759,25 +778,21 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       } else {
         if (lane == 0) dst->sums = b;
         if (kTop) dst->keys[lane] = l;
-        __syncwarp();
       }
+      __syncwarp();
     }
-    __syncwarp();
+    if (warp == 0) {
+      const bool now = whole && on, before = turn && part == 0 && ent_prev >= 0;
+      if (now || before)
+        finish(now ? buf : buf ^ 1, now ? 1 : C, now ? ent : ent_prev, now ? xt : xt_prev, now ? st : st_prev);
+      __syncwarp();
+    }
     ent_prev = on ? ent : -1;
     st_prev = st;
     xt_prev = xt;
-    if (!whole && C > 1) {
-      cluster_arrive();
-    } else if (warp == 0 && on) {
-      finish(buf, 1);
-      __syncwarp();
-    }
+    if (C > 1 && it >= waves && it < rows) cluster_arrive();
   }
   copy_wait<0>();
-  if (C > 1) {
-    cluster_wait();
-    if (part == 0 && warp == 0 && ent_prev >= 0) finish((rows - 1) & 1, C);
-  }
 }
 
 template <bool kBF16, bool kTop>
@@ -830,18 +845,48 @@ template <bool kBF16, bool kTop>
 static int launch_t(LogprobsParams p, cudaStream_t stream) {
   // slices of at least 4 KB; no more CTAs than the rows can use
   const int elt = kBF16 ? 2 : 4;
-  // a row shared by many CTAs for latency while the rows are few (or may be: a
-  // node list usually selects a path); smaller clusters leave fewer SMs unused
-  int cluster = p.nodes || (long long)p.B * p.M * kMaxC <= sm_count() * 3 ? kMaxC : 4;
-  while (cluster > 1 && (long long)p.V * elt < 4096LL * cluster) cluster >>= 1;
+  const long long all = (long long)p.B * p.M;
   int slots = 0;
-  for (;; cluster >>= 1) {
-    slots = resident_ctas<kBF16, kTop>(cluster);
-    if (slots < 0) return DDT_ERR_CUDA;
-    if (slots > 0 || cluster == 1) break;
+  auto fit = [&](int& cluster) {  // the largest cluster up to this one that can be scheduled, with slices of 4 KB
+    while (cluster > 1 && (long long)p.V * elt < 4096LL * cluster) cluster >>= 1;
+    for (;; cluster >>= 1) {
+      slots = resident_ctas<kBF16, kTop>(cluster);
+      if (slots != 0 || cluster == 1) break;
+    }
+    if (slots == 0) slots = 3 * sm_count();
+  };
+  // A node list selects few rows as a rule: clusters of 8, the split decided
+  // on the device. All rows: clusters of 4 (they leave fewer SMs unused) and
+  // full waves if the rows fill the device; fewer rows are split so that one
+  // wave of CTAs lies evenly on the SMs. One CTA alone keeps an SM about 45 %
+  // busy, two 80 %.
+  int cluster = p.nodes ? kMaxC : 4;
+  fit(cluster);
+  p.log_share = -1;
+  if (!p.nodes && all < slots) {
+    static const float load[4] = {0.0f, 2.2f, 2.5f, 3.0f};
+    const float fixed = kTop ? 0.2f : 0.05f;  // of a row's time, per slice
+    float best = -1.0f;
+    int pick = 1;
+    for (int l = 0; l < 4; ++l) {
+      int c = 1 << l;
+      fit(c);
+      if (slots < 0) return DDT_ERR_CUDA;
+      const long long ctas = all << l;
+      if (c != 1 << l || ctas > slots) break;
+      const float cost = load[std::min(3LL, (ctas + sm_count() - 1) / sm_count())] * (1.0f / c + fixed);
+      if (best < 0.0f || cost < best) {
+        best = cost;
+        pick = c;
+        p.log_share = l;
+      }
+    }
+    cluster = pick;
+    slots = (int)all * cluster;
   }
-  const long long most = std::max(1, (slots > 0 ? slots : 3 * sm_count()) / cluster);
+  if (slots < 0) return DDT_ERR_CUDA;
   p.cluster = cluster;
+  const long long most = std::max(1, slots / cluster);
   const long long total = (long long)p.B * p.M;
   const long long step = p.nodes ? kListMax : total;
   for (long long e0 = 0; e0 < total; e0 += step) {
