@@ -64,8 +64,9 @@ constexpr int kRingBytes = kStages * kRound * 16;
 constexpr int kMaxC = 8;          // CTAs that may share a row
 constexpr int kListMax = 1024;    // entries of a launch that follows a node list
 constexpr int kStep = 64;         // threads that add keys between two looks in the careful pass
-constexpr int kCand = 256 + kStep * 8;  // keys of the CTA's buffer
-constexpr int kPick = kCand;      // of these, the ones that reach the final bound
+constexpr int kWarpCand = 96;     // keys of a warp's buffer
+constexpr int kCand = kWarps * kWarpCand;
+constexpr int kPick = 128;        // of these, the ones that reach the final bound
 constexpr float kFar = -150.0f;   // e^kFar and 2^kFar are zero in float32
 constexpr float kUsual = 1e6f;    // below this, a logit in base 2 is off by less than one before it is rounded
 constexpr float kLn2 = 0.6931471805599453f;
@@ -143,10 +144,20 @@ __device__ __forceinline__ Sums join(Sums a) {
   return a;
 }
 
+// How many of n keys in shared memory are larger than this one (keys differ):
+// its place among them. Independent broadcasts and compares, a third of a
+// sorting network's latency for the 10 to 40 keys that are left.
+__device__ __forceinline__ int rank_of(unsigned long long key, const unsigned long long* keys, int n) {
+  int r = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) r += keys[i] > key ? 1 : 0;
+  return r;
+}
+
 struct Part {  // one CTA's share of a row
   Sums sums;
-  float pad;
-  unsigned long long keys[32];
+  float bound;                  // at least K values of the row reach it
+  unsigned long long keys[32];  // its best keys (0: none), in any order
 };
 
 template <bool kBF16>
@@ -182,6 +193,7 @@ struct Max;
 template <>
 struct Max<true> {
   __nv_bfloat162 v;
+  __device__ __forceinline__ Max() {}
   __device__ __forceinline__ static __nv_bfloat162 h(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   __device__ __forceinline__ explicit Max(const uint4& r) : v(__hmax2_nan(__hmax2_nan(h(r.x), h(r.y)), __hmax2_nan(h(r.z), h(r.w)))) {}
   __device__ __forceinline__ void add(const Max& o) { v = __hmax2_nan(v, o.v); }
@@ -190,6 +202,7 @@ struct Max<true> {
 template <>
 struct Max<false> {
   float v;
+  __device__ __forceinline__ Max() {}
   __device__ __forceinline__ explicit Max(const uint4& r) {
     v = max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)), max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
@@ -218,8 +231,8 @@ __device__ __noinline__ uint4 load_edge(const unsigned char* row, int V, int ful
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Appends the keys of a vector's values that reach T (T's value: tv) to the
-// CTA's buffer. A key that finds the buffer full is lost, but counted.
+// Careful pass: appends the keys of a vector's values that reach T (T's value:
+// tv) to the CTA's buffer.
 template <bool kBF16>
 __device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, float tv, unsigned long long* cand,
                                          int* count) {
@@ -340,8 +353,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   __shared__ __align__(16) Part s_part[2][kMaxC];
   __shared__ unsigned long long s_cand[kTop ? kCand : 1];
   __shared__ unsigned long long s_lists[kTop ? kWarps : 1][32];
-  __shared__ unsigned long long s_pick[kTop ? kPick : 1];
-  __shared__ int s_count[2], s_picked;
+  __shared__ unsigned long long s_pick[kTop ? kPick : 1], s_last[kTop ? kMaxC * 32 : 1];
+  __shared__ int s_count[2], s_picked[3];  // by the row's number; s_picked is read after the row's last barrier
+  __shared__ uint4 s_ends[2];
   __shared__ uint32_t s_bound[2][kWarps];  // by the row's parity: the warps' j-th largest values, 0 for none
   constexpr int kPer = Vec<kBF16>::kPer;
   constexpr int kElt = kBF16 ? 2 : 4;
@@ -518,34 +532,79 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       if (p.dev_status) p.dev_status[entry] = bad ? DDT_ERR_INPUT : DDT_OK;
     }
     if (kTop) {
-      unsigned long long best = q[0].keys[lane];
+      // the slices' keys that reach the best of their bounds, by rank
+      float tv = lane < c ? q[lane].bound : -INFINITY;
+#pragma unroll
+      for (int o = kMaxC / 2; o > 0; o >>= 1) tv = fmaxf(tv, __shfl_xor_sync(DDT_FULL_MASK, tv, o));
+      tv = __shfl_sync(DDT_FULL_MASK, tv, 0);
+      int n = 0;
 #pragma unroll 1
-      for (int r = 1; r < c; ++r) best = merge_lists(best, q[r].keys[lane], lane);
-      if (lane < K) {
-        const bool has = !bad && best != 0ull;
-        p.top_logp[entry * K + lane] = has ? (key_value(best) - a.m) - lns : -INFINITY;
-        p.top_tok[entry * K + lane] = has ? static_cast<int32_t>(~static_cast<uint32_t>(best)) : -1;
+      for (int r = 0; r < c; ++r) {
+        const unsigned long long key = q[r].keys[lane];
+        const bool keep = !bad && key != 0ull && key_value(key) >= tv;
+        const unsigned votes = __ballot_sync(DDT_FULL_MASK, keep);
+        if (keep) s_last[n + __popc(votes & ((1u << lane) - 1u))] = key;
+        n += __popc(votes);
+      }
+      __syncwarp();
+      if (n > 32 && K <= 8) {
+        // shared rows: about K from every slice. The K-th largest of the
+        // lanes' largest values leaves few more than K of them
+        uint32_t x = 0u, top = 0u;
+        for (int i = lane; i < n; i += 32) x = max(x, (uint32_t)(s_last[i] >> 32));
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+          top = __reduce_max_sync(DDT_FULL_MASK, x);
+          const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
+          if (lane == __ffs(who) - 1) x = 0u;
+        }
+        int left = 0;
+        for (int i = 0; i < n; i += 32) {  // in place: a key moves to its place or a lower one
+          const unsigned long long key = i + lane < n ? s_last[i + lane] : 0ull;
+          const bool keep = key != 0ull && (uint32_t)(key >> 32) >= top;
+          const unsigned votes = __ballot_sync(DDT_FULL_MASK, keep);
+          if (keep) s_last[left + __popc(votes & ((1u << lane) - 1u))] = key;
+          left += __popc(votes);
+          __syncwarp();
+        }
+        n = left;
+      }
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) {
+        const unsigned long long key = s_last[i];
+        const int r = rank_of(key, s_last, n);
+        if (r < K) {
+          p.top_logp[entry * K + r] = (key_value(key) - a.m) - lns;
+          p.top_tok[entry * K + r] = static_cast<int32_t>(~static_cast<uint32_t>(key));
+        }
+      }
+      for (int r = n + lane; r < K; r += 32) {  // fewer tokens than K are possible
+        p.top_logp[entry * K + r] = -INFINITY;
+        p.top_tok[entry * K + r] = -1;
       }
     }
   };
 
   if (kTop) {
     if (tid < 2 * kWarps) s_bound[tid / kWarps][tid % kWarps] = 0u;
-    if (tid == 0) s_count[0] = s_count[1] = s_picked = 0;
+    if (tid == 0) s_count[0] = s_count[1] = s_picked[0] = s_picked[1] = s_picked[2] = 0;
     __syncthreads();
   }
+  int turn3 = 2;  // it mod 3
 #pragma unroll 1
   for (int it = 0; it < rows + (C > 1 ? 1 : 0); ++it) {  // shared rows are joined a turn later
     const bool whole = it < waves || C == 1;  // this CTA has the whole row
     const int buf = it & 1;
+    turn3 = turn3 == 2 ? 0 : turn3 + 1;
     long long ent;
     const unsigned char* row;
     locate(it, ent, row);
     const bool on = ent >= 0;  // the same for the CTAs of a group
     Sums a = {-INFINITY, 0.0f, 0.0f};
+    float tv = -INFINITY;  // at least K values of the slice reach it
     if (kTop) {  // the next row's; nobody uses them before this row's barriers
       if (lane == 0) s_bound[buf ^ 1][warp] = 0u;
-      if (tid == 0) s_count[buf ^ 1] = 0;
+      if (tid == 0) s_count[buf ^ 1] = s_picked[turn3 == 2 ? 0 : turn3 + 1] = 0;
     }
     if (on) {
       const int t = __ldg(p.tok + ent);
@@ -570,7 +629,6 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         // moves it.
         uint64_t s2 = 0ull, u2 = 0ull;
         float ref = 0.0f, limit = -INFINITY;
-        float tv = -INFINITY;  // at least K values of the slice reach it
         const int first = min(kThreads, max(v1 - v0, ends ? 2 : 0));  // threads with values in round 0
         const int tr = max(1, min(min(K, 4), (first + 31) / 32)), tj = tr == 1 ? K : tr == 2 ? (K + 1) >> 1 : tr == 4 ? (K + 3) >> 2 : (K + 2) / 3;
         // this warp's tj-th largest of its threads' largest values
@@ -651,8 +709,14 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
             }
           }
         };
-        // one round's alternatives; at: element of this thread's first value
-        auto top = [&](const uint4 (&v)[kU], float rm, int r, int at) {
+        int mine = 0;  // keys this warp appended to its buffer
+        // One round's alternatives: the vectors whose largest value (vm) reaches
+        // the bound are looked at once more where they lie in shared memory,
+        // `from` the first of this thread's; `at` is its first element. The
+        // warp's lanes append together: a place in the warp's buffer is a vote
+        // and a count, no atomics. Keys beyond the buffer's end are lost, but
+        // counted.
+        auto top = [&](const Max<kBF16> (&vm)[kU], float rm, int r, const unsigned char* from, int at) {
           if (r == 0 || r == 2 || r == 8) {
             publish();
             if (r == 0) __syncthreads();  // a first bound needs every warp's
@@ -660,17 +724,43 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
           } else if (r == 1 || (r & 3) == 0) {
             bound();
           }
-          if (rm >= tv && rm > -INFINITY) {
+          if (!__any_sync(DDT_FULL_MASK, rm >= tv && rm > -INFINITY)) return;
+          unsigned um = 0u;
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
-              if (Max<kBF16>(v[u]).value() >= tv)
-                append_keys<kBF16>(v[u], at + u * kThreads * kPer, 0ull, tv, s_cand, &s_count[buf]);
+          for (int u = 0; u < kU; ++u) {
+            const float x = vm[u].value();
+            um |= x >= tv && x > -INFINITY ? 1u << u : 0u;
+          }
+          while (__any_sync(DDT_FULL_MASK, um != 0u)) {
+            const int u = um ? __ffs(um) - 1 : 0;
+            const unsigned char* vec = from + u * kThreads * 16;
+            const uint4 x = *reinterpret_cast<const uint4*>(vec);
+            unsigned hits = 0u;
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) hits |= value_of<kBF16>(x, q) >= tv ? 1u << q : 0u;
+            if (um == 0u) hits = 0u;
+            um &= um - 1u;
+            unsigned votes;
+            while ((votes = __ballot_sync(DDT_FULL_MASK, hits != 0u)) != 0u) {
+              const int q = hits ? __ffs(hits) - 1 : 0;
+              const float y = kBF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(vec)[q])
+                                    : reinterpret_cast<const float*>(vec)[q];
+              const int place = mine + __popc(votes & ((1u << lane) - 1u));
+              if (hits && place < kWarpCand)
+                s_cand[warp * kWarpCand + place] = y > -INFINITY ? topk_key(y, at + u * kThreads * kPer + q) : 0ull;
+              mine += __popc(votes);
+              hits &= hits - 1u;
+            }
           }
         };
-        auto largest = [&](const uint4 (&v)[kU]) {
+        auto largest = [&](const uint4 (&v)[kU], Max<kBF16> (&vm)[kU]) {
           Max<kBF16> m(v[0]);
+          vm[0] = m;
 #pragma unroll
-          for (int u = 1; u < kU; ++u) m.add(Max<kBF16>(v[u]));
+          for (int u = 1; u < kU; ++u) {
+            vm[u] = Max<kBF16>(v[u]);
+            m.add(vm[u]);
+          }
           return m.value();
         };
         auto next_slot = [&](uint32_t x) { return x >= (kStages - 1) * kRound * 16 ? x - (kStages - 1) * kRound * 16 : x + kRound * 16; };
@@ -684,12 +774,13 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
 #pragma unroll
           for (int u = 0; u < kU; ++u) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
           slot = next_slot(slot);
-          const float rm = largest(v);
-          // this round's vectors are in registers: their slots are free
+          Max<kBF16> vm[kU];
+          const float rm = largest(v, vm);
+          sums(v, rm);
+          if (kTop) top(vm, rm, r, from, at);
+          // this round's slots are free
           if (f_left >= kRound) fetch_round();
           else fetch();
-          sums(v, rm);
-          if (kTop) top(v, rm, r, at);
         }
 #pragma unroll 1
         for (; left > 0 || ends; left -= kRound, ++r, at += kRound * kPer) {
@@ -697,40 +788,50 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
 #pragma unroll
           for (int u = 0; u < kU; ++u) v[u] = none;
           int pos = at;
+          const unsigned char* from = s_ring + slot;
           if (left > 0) {
             copy_wait<kStages - 1>();
-            const unsigned char* from = s_ring + slot;
 #pragma unroll
             for (int u = 0; u < kU; ++u)
               if (left > tid + u * kThreads) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
             slot = next_slot(slot);
           } else {  // the row's ends
             ends = false;
-            if (tid < 2) v[0] = load_edge<kBF16>(row, V, full0, full1, tid);
-            pos = tid == 0 ? full0 - kPer : full1;
+            if (tid < 2) {
+              v[0] = load_edge<kBF16>(row, V, full0, full1, tid);
+              s_ends[tid] = v[0];
+              from = reinterpret_cast<const unsigned char*>(&s_ends[tid]);
+              pos = tid == 0 ? full0 - kPer : full1;
+            }
           }
-          const float rm = largest(v);
-          if (left > 0) fetch();
+          Max<kBF16> vm[kU];
+          const float rm = largest(v, vm);
           sums(v, rm);
-          if (kTop) top(v, rm, r, pos);
+          if (kTop) top(vm, rm, r, from, pos);
+          if (left > 0) fetch();
         }
         if (kTop) {
-          // of the buffer, the keys that reach the final bound: few more than K
+          // of the warps' buffers, the keys that reach the final bound: few
+          // more than K
           if (r > 0) publish();
+          if (lane == 0 && mine > kWarpCand) s_count[buf] = kCand + 1;
           __syncthreads();
           bound();
-          int n = s_count[buf];
-          if (n > kCand) {  // keys were lost: the same for the whole CTA
+          int n = min(mine, kWarpCand), from = warp * kWarpCand;
+          if (s_count[buf] > kCand) {  // keys were lost: the same for the whole CTA
             careful_keys<kBF16>(row, V, full0, full1, v0, v1, has_ends, K, s_cand, &s_count[buf], s_lists);
-            n = 32;
+            n = warp == 0 ? 32 : 0;
+            from = 0;
             tv = -INFINITY;
           }
-          for (int i = tid; i < n; i += kThreads) {
-            const unsigned long long key = s_cand[i];
-            if (key != 0ull && key_value(key) >= tv) {
-              const int at = atomicAdd(&s_picked, 1);
-              if (at < kPick) s_pick[at] = key;
-            }
+          for (int i = 0; i < n; i += 32) {
+            const unsigned long long key = i + lane < n ? s_cand[from + i + lane] : 0ull;
+            const bool keep = key != 0ull && key_value(key) >= tv;
+            const unsigned votes = __ballot_sync(DDT_FULL_MASK, keep);
+            int at = 0;
+            if (lane == 0 && votes) at = atomicAdd(&s_picked[turn3], __popc(votes));
+            at = __shfl_sync(DDT_FULL_MASK, at, 0) + __popc(votes & ((1u << lane) - 1u));
+            if (keep && at < kPick) s_pick[at] = key;
           }
         }
         float s0, s1, u0, u1;
@@ -748,16 +849,20 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       if (lane == 0) s_sums[buf][warp] = a;
     }
     __syncthreads();
-    unsigned long long l = 0ull;  // warp 0: the slice's best keys over the lanes
-    if (kTop && warp == 0) {
-      const int n = s_picked;
-#pragma unroll 1
-      for (int c = 0; c < n; c += 32) {
-        const unsigned long long x = sort_list(c + lane < n ? s_pick[c + lane] : 0ull, lane);
-        l = c == 0 ? x : merge_lists(l, x, lane);
-      }
-      __syncwarp();
-      if (lane == 0) s_picked = 0;
+    if (kTop && on && s_picked[turn3] > kPick) {  // many equal values: the same for the whole CTA
+      long long e2;
+      const unsigned char* row2;
+      locate(it, e2, row2);
+      int full0, nfull, v0, v1;
+      shape(row2, full0, nfull);
+      share(it, nfull, v0, v1);
+      const int full1 = full0 + nfull * kPer;
+      careful_keys<kBF16>(row2, V, full0, full1, v0, v1, (full0 > 0 || full1 < V) && (whole || part == 0), K, s_cand,
+                          &s_count[buf], s_lists);
+      if (warp == 0) s_pick[lane] = s_cand[lane];
+      if (tid == 0) s_picked[turn3] = 32;
+      tv = -INFINITY;
+      __syncthreads();
     }
     // the shared row before this one is complete in the group's first CTA
     __syncwarp();
@@ -767,17 +872,23 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       const Sums b = join<kWarps>(lane < kWarps ? s_sums[buf][lane] : Sums{-INFINITY, 0.0f, 0.0f});
       const int to = whole ? 0 : part;
       Part* dst = &s_part[buf][to];
-      if (to != 0) {
-        const uint32_t base = map_to_rank(smem_u32(dst), (uint32_t)lead);
-        if (lane == 0) {
-          st_cluster_f32(base, b.m);
-          st_cluster_f32(base + 4, b.s);
-          st_cluster_f32(base + 8, b.u);
+      // the slice's keys: all that are left if that is at most 32, else the 32 best
+      const int n = kTop ? s_picked[turn3] : 0;
+      const uint32_t base = map_to_rank(smem_u32(dst), (uint32_t)(to != 0 ? lead : crank));
+      if (lane == 0) {
+        st_cluster_f32(base, b.m);
+        st_cluster_f32(base + 4, b.s);
+        st_cluster_f32(base + 8, b.u);
+        st_cluster_f32(base + 12, tv);
+      }
+      if (kTop && n <= 32) {
+        st_cluster_u64(base + 16 + 8 * lane, lane < n ? s_pick[lane] : 0ull);
+      } else if (kTop) {
+        for (int i = lane; i < n; i += 32) {
+          const unsigned long long key = s_pick[i];
+          const int r = rank_of(key, s_pick, n);
+          if (r < 32) st_cluster_u64(base + 16 + 8 * r, key);
         }
-        if (kTop) st_cluster_u64(base + 16 + 8 * lane, l);
-      } else {
-        if (lane == 0) dst->sums = b;
-        if (kTop) dst->keys[lane] = l;
       }
       __syncwarp();
     }
