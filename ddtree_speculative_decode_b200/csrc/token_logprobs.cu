@@ -64,6 +64,7 @@ constexpr int kRingBytes = kStages * kRound * 16;
 constexpr int kMaxC = 8;          // CTAs that may share a row
 constexpr int kListMax = 1024;    // entries of a launch that follows a node list
 constexpr int kStep = 64;         // threads that add keys between two looks in the careful pass
+constexpr int kBest = 4;          // warps whose published values make the bound
 constexpr int kWarpCand = 96;     // keys of a warp's buffer
 constexpr int kCand = kWarps * kWarpCand;
 constexpr int kPick = 128;        // of these, the ones that reach the final bound
@@ -76,6 +77,9 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -156,7 +160,8 @@ __device__ __forceinline__ int rank_of(unsigned long long key, const unsigned lo
 
 struct Part {  // one CTA's share of a row
   Sums sums;
-  float bound;                  // at least K values of the row reach it
+  float pad;
+  uint32_t bounds[kWarps];      // its warps' published values
   unsigned long long keys[32];  // its best keys (0: none), in any order
 };
 
@@ -343,6 +348,21 @@ __device__ __noinline__ void careful_keys(const unsigned char* row, int V, int f
   __syncthreads();
 }
 
+// The r-th largest of the warps' published values (0 if fewer are published).
+__device__ __forceinline__ uint32_t nth_largest(const uint32_t* values, int r, int lane) {
+  const volatile uint32_t* v = values;
+  const uint32_t x = v[lane % kWarps];
+  int more = 0, same = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const uint32_t y = __shfl_sync(DDT_FULL_MASK, x, i);
+    more += y > x ? 1 : 0;
+    same += y == x ? 1 : 0;
+  }
+  const unsigned who = __ballot_sync(DDT_FULL_MASK, more < r && more + same >= r);
+  return __shfl_sync(DDT_FULL_MASK, x, __ffs(who) - 1);
+}
+
 template <bool kBF16, bool kTop>
 __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsParams p) {
   extern __shared__ __align__(16) unsigned char s_ring[];  // [kStages][kU][kThreads] vectors
@@ -356,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   __shared__ unsigned long long s_pick[kTop ? kPick : 1], s_last[kTop ? kMaxC * 32 : 1];
   __shared__ int s_count[2], s_picked[3];  // by the row's number; s_picked is read after the row's last barrier
   __shared__ uint4 s_ends[2];
-  __shared__ uint32_t s_bound[2][kWarps];  // by the row's parity: the warps' j-th largest values, 0 for none
+  __shared__ __align__(16) uint32_t s_bound[2][kWarps];  // by the row's parity: the warps' j-th largest values, 0 for none
   constexpr int kPer = Vec<kBF16>::kPer;
   constexpr int kElt = kBF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -532,43 +552,37 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       if (p.dev_status) p.dev_status[entry] = bad ? DDT_ERR_INPUT : DDT_OK;
     }
     if (kTop) {
-      // the slices' keys that reach the best of their bounds, by rank
-      float tv = lane < c ? q[lane].bound : -INFINITY;
-#pragma unroll
-      for (int o = kMaxC / 2; o > 0; o >>= 1) tv = fmaxf(tv, __shfl_xor_sync(DDT_FULL_MASK, tv, o));
-      tv = __shfl_sync(DDT_FULL_MASK, tv, 0);
-      int n = 0;
+      // The bound of the whole row, from the warps of all its slices (at
+      // least min(K, kBest) of them publish, unless the row is short), and the
+      // keys that reach it: about K. Independent steps throughout: this is
+      // the end of a row's latency.
+      uint32_t x0 = lane < 4 * c ? q[lane >> 2].bounds[(lane & 3) * 2] : 0u;
+      uint32_t x1 = lane < 4 * c ? q[lane >> 2].bounds[(lane & 3) * 2 + 1] : 0u;
+      const int full = __popc(__ballot_sync(DDT_FULL_MASK, x0 != 0u)) + __popc(__ballot_sync(DDT_FULL_MASK, x1 != 0u));
+      // every warp's value is its j-th largest with j >= ceil(K / kBest)
+      const int need = min(K, kBest);
+      uint32_t top = 0u;
+      if (full >= need) {
 #pragma unroll 1
-      for (int r = 0; r < c; ++r) {
-        const unsigned long long key = q[r].keys[lane];
-        const bool keep = !bad && key != 0ull && key_value(key) >= tv;
+        for (int i = 0; i < need; ++i) {
+          top = __reduce_max_sync(DDT_FULL_MASK, max(x0, x1));
+          const unsigned who = __ballot_sync(DDT_FULL_MASK, max(x0, x1) == top);
+          if (lane == __ffs(who) - 1) {
+            if (x0 >= x1) x0 = 0u;
+            else x1 = 0u;
+          }
+        }
+      }
+      int n = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxC; ++r) {
+        const unsigned long long key = r < c ? q[r].keys[lane] : 0ull;
+        const bool keep = !bad && key != 0ull && (uint32_t)(key >> 32) >= top;
         const unsigned votes = __ballot_sync(DDT_FULL_MASK, keep);
         if (keep) s_last[n + __popc(votes & ((1u << lane) - 1u))] = key;
         n += __popc(votes);
       }
       __syncwarp();
-      if (n > 32 && K <= 8) {
-        // shared rows: about K from every slice. The K-th largest of the
-        // lanes' largest values leaves few more than K of them
-        uint32_t x = 0u, top = 0u;
-        for (int i = lane; i < n; i += 32) x = max(x, (uint32_t)(s_last[i] >> 32));
-#pragma unroll 1
-        for (int k = 0; k < K; ++k) {
-          top = __reduce_max_sync(DDT_FULL_MASK, x);
-          const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
-          if (lane == __ffs(who) - 1) x = 0u;
-        }
-        int left = 0;
-        for (int i = 0; i < n; i += 32) {  // in place: a key moves to its place or a lower one
-          const unsigned long long key = i + lane < n ? s_last[i + lane] : 0ull;
-          const bool keep = key != 0ull && (uint32_t)(key >> 32) >= top;
-          const unsigned votes = __ballot_sync(DDT_FULL_MASK, keep);
-          if (keep) s_last[left + __popc(votes & ((1u << lane) - 1u))] = key;
-          left += __popc(votes);
-          __syncwarp();
-        }
-        n = left;
-      }
 #pragma unroll 1
       for (int i = lane; i < n; i += 32) {
         const unsigned long long key = s_last[i];
@@ -602,19 +616,15 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     const bool on = ent >= 0;  // the same for the CTAs of a group
     Sums a = {-INFINITY, 0.0f, 0.0f};
     float tv = -INFINITY;  // at least K values of the slice reach it
+    bool plain = true;     // the buffers held every key that reaches it
     if (kTop) {  // the next row's; nobody uses them before this row's barriers
       if (lane == 0) s_bound[buf ^ 1][warp] = 0u;
       if (tid == 0) s_count[buf ^ 1] = s_picked[turn3 == 2 ? 0 : turn3 + 1] = 0;
     }
     if (on) {
       const int t = __ldg(p.tok + ent);
-      st = row && t >= 0 && t < V ? DDT_OK : DDT_ERR_INPUT;
+      st = DDT_ERR_INPUT;
       if (row) {
-        if ((whole || part == 0) && warp == 0) {
-          xt = 0.0f;
-          if (st == DDT_OK) xt = kBF16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + t))
-                                       : __ldg(reinterpret_cast<const float*>(row) + t);
-        }
         int full0, nfull, v0, v1;
         shape(row, full0, nfull);
         share(it, nfull, v0, v1);
@@ -630,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         uint64_t s2 = 0ull, u2 = 0ull;
         float ref = 0.0f, limit = -INFINITY;
         const int first = min(kThreads, max(v1 - v0, ends ? 2 : 0));  // threads with values in round 0
-        const int tr = max(1, min(min(K, 4), (first + 31) / 32)), tj = tr == 1 ? K : tr == 2 ? (K + 1) >> 1 : tr == 4 ? (K + 3) >> 2 : (K + 2) / 3;
+        const int tr = max(1, min(min(K, kBest), (first + 31) / 32)), tj = (K + tr - 1) / tr;
         // this warp's tj-th largest of its threads' largest values
         auto publish = [&]() {
           uint32_t x = a.m > -INFINITY ? float_order_key(a.m) : 0u, top = 0u;
@@ -642,16 +652,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
           }
           if (lane == 0) *const_cast<volatile uint32_t*>(&s_bound[buf][warp]) = top;
         };
-        // the tr-th largest of the warps' published values
         auto bound = [&]() {
-          uint32_t x = lane < kWarps ? *const_cast<volatile uint32_t*>(&s_bound[buf][lane]) : 0u, top = 0u;
-#pragma unroll 1
-          for (int q = 0; q < tr; ++q) {
-            top = __reduce_max_sync(DDT_FULL_MASK, x);
-            const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
-            if (lane == __ffs(who) - 1) x = 0u;
-          }
-          if (top != 0u) tv = fmaxf(tv, key_value((unsigned long long)top << 32));
+          const uint32_t t = nth_largest(s_bound[buf], tr, lane);
+          if (t != 0u) tv = fmaxf(tv, key_value((unsigned long long)t << 32));
         };
         // one round's sums; rm: the largest of its values (NaN if one is)
         auto sums = [&](const uint4 (&v)[kU], float rm) {
@@ -810,6 +813,14 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
           if (kTop) top(vm, rm, r, from, pos);
           if (left > 0) fetch();
         }
+        // the given token's logit: its index has arrived by now, and the join
+        // wants it much later
+        st = t >= 0 && t < V ? DDT_OK : DDT_ERR_INPUT;
+        if ((whole || part == 0) && warp == 0) {
+          xt = 0.0f;
+          if (st == DDT_OK) xt = kBF16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + t))
+                                       : __ldg(reinterpret_cast<const float*>(row) + t);
+        }
         if (kTop) {
           // of the warps' buffers, the keys that reach the final bound: few
           // more than K
@@ -823,6 +834,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
             n = warp == 0 ? 32 : 0;
             from = 0;
             tv = -INFINITY;
+            plain = false;
           }
           for (int i = 0; i < n; i += 32) {
             const unsigned long long key = i + lane < n ? s_cand[from + i + lane] : 0ull;
@@ -861,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
                           &s_count[buf], s_lists);
       if (warp == 0) s_pick[lane] = s_cand[lane];
       if (tid == 0) s_picked[turn3] = 32;
-      tv = -INFINITY;
+      plain = false;
       __syncthreads();
     }
     // the shared row before this one is complete in the group's first CTA
@@ -879,15 +891,15 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         st_cluster_f32(base, b.m);
         st_cluster_f32(base + 4, b.s);
         st_cluster_f32(base + 8, b.u);
-        st_cluster_f32(base + 12, tv);
       }
+      if (kTop && lane < kWarps) st_cluster_u32(base + 16 + 4 * lane, plain ? s_bound[buf][lane] : 0u);
       if (kTop && n <= 32) {
-        st_cluster_u64(base + 16 + 8 * lane, lane < n ? s_pick[lane] : 0ull);
+        st_cluster_u64(base + 16 + 4 * kWarps + 8 * lane, lane < n ? s_pick[lane] : 0ull);
       } else if (kTop) {
         for (int i = lane; i < n; i += 32) {
           const unsigned long long key = s_pick[i];
           const int r = rank_of(key, s_pick, n);
-          if (r < 32) st_cluster_u64(base + 16 + 8 * r, key);
+          if (r < 32) st_cluster_u64(base + 16 + 4 * kWarps + 8 * r, key);
         }
       }
       __syncwarp();
