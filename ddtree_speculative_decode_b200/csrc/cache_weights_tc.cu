@@ -13,8 +13,9 @@
 // An item is 256 keys of one request (a CTA pair, 128 keys per CTA, tcgen05
 // cta_group::2, M = 256) times the request's query rows, or a share of them.
 // The CTA's 128 keys stay in shared memory for the item (d / 64 slabs of 16
-// KB), the query rows stream through a ring of 16 KB stages (half of a tile's
-// up to 256 rows x 64 dims each, the pair holds the other half), fetched by
+// KB), the query rows stream through a ring of stages (half of a tile's up
+// to 256 rows x 64 dims each, the pair holds the other half; 4 stages of 16 KB,
+// more smaller ones when the tiles are small), fetched by
 // node from the caller's list: a unit is a node's heads or an even share of
 // them (padded to 8 rows, at most 128), which are consecutive rows of q.
 // Slabs are released one by one behind the item's last tile, so the next
@@ -47,27 +48,27 @@ using namespace sm100;
 constexpr int kThreads = 320;        // warp 0 TMA, warp 1 MMA + TMEM, warps 2..9 weights
 constexpr int kSlabBytes = 128 * 128;  // 128 rows x 64 dims bf16
 constexpr int kMaxSlabs = 9;
-constexpr int kStages = 4;
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 4 * kSlabBytes;  // stages of query rows
 constexpr int kMaxB = 256;           // requests of one launch
 constexpr int kMaxShares = 16;
 constexpr int kMaxParts = 320;       // (key tile, share) partials of a split launch
 
 constexpr int kBarAFull = 0;                          // [kMaxSlabs] leader: a slab of keys (both CTAs)
 constexpr int kBarAEmpty = kBarAFull + kMaxSlabs;     // [kMaxSlabs] each CTA: the item's MMAs are done with it
-constexpr int kBarBFull = kBarAEmpty + kMaxSlabs;     // [kStages] leader: a stage of query rows
-constexpr int kBarBEmpty = kBarBFull + kStages;       // [kStages] each CTA
-constexpr int kBarAccFull = kBarBEmpty + kStages;     // [2] each CTA
+constexpr int kBarBFull = kBarAEmpty + kMaxSlabs;     // [kMaxStages] leader: a stage of query rows
+constexpr int kBarBEmpty = kBarBFull + kMaxStages;    // [kMaxStages] each CTA
+constexpr int kBarAccFull = kBarBEmpty + kMaxStages;     // [2] each CTA
 constexpr int kBarAccEmpty = kBarAccFull + 2;         // [2] leader: read by 8 warps x 2 CTAs
 constexpr int kNumBars = kBarAccEmpty + 2;
 
 struct Shared {  // behind the slabs and stages
-  unsigned long long bars[kNumBars + 1];
+  unsigned long long bars[kNumBars];
   uint32_t tmem;
   int aborted;
   int shares, total, last;
-  int pad;
-  float lse2[2][256];
-  int sees[2][256];
+  alignas(16) float lse2[2][256];
+  alignas(16) int sees[2][256];
   float half[128];
   int len[kMaxB];        // -1: the request is skipped
   int m[kMaxB];          // entries of its list
@@ -82,6 +83,7 @@ struct Params {
   int unit;              // query rows of one unit (a multiple of 8, at most 128)
   int chunks;            // units per node
   int per_half;          // units that fit half a tile's 128 columns
+  int stages, stage_bytes;  // of the ring of query rows
   float sl2;             // scale log2 e
   int* abort;
   unsigned* counters;    // [kMaxParts][2] arrivals, zero between calls
@@ -106,30 +108,40 @@ __device__ __forceinline__ bool bar_red_and(int id, int nthreads, bool pred) {
 struct Cursor {
   int item, b;
   __device__ explicit Cursor(int first) : item(first), b(0) {}
-  // false: no more items. Else the request, its key tile and the query tiles
-  // [t0, t1) of this share.
-  __device__ bool get(const Shared& s, const Params& p, int& kt, int& share, int& nshare, int& t0, int& t1) {
+  // false: no more items. Else the request, its key tile and the share's units
+  // [u0, u1), dealt in tiles of `per` units.
+  __device__ bool get(const Shared& s, const Params& p, int& kt, int& share, int& nshare, int& u0, int& u1, int& per) {
     if (item >= s.total) return false;
     while (item >= s.item0[b + 1]) ++b;
-    const int units = s.m[b] * p.chunks, per = 2 * p.per_half;
-    const int qt = (units + per - 1) / per;
-    nshare = max(1, min(s.shares, qt));
-    const int i = item - s.item0[b];
-    kt = i / nshare;
-    share = i - kt * nshare;
-    t0 = (int)((long long)qt * share / nshare);
-    t1 = (int)((long long)qt * (share + 1) / nshare);
+    const int units = s.m[b] * p.chunks;
+    nshare = max(1, min(s.shares, units));
+    kt = item - s.item0[b];
+    share = 0;
+    u0 = 0;
+    u1 = units;
+    if (nshare > 1) {
+      share = kt % nshare;
+      kt /= nshare;
+      const int base = units / nshare, more = units - base * nshare;
+      u0 = share * base + min(share, more);
+      u1 = u0 + base + (share < more ? 1 : 0);
+    }
+    const int most = 2 * p.per_half, n = u1 - u0;
+    per = n;
+    if (n > most) {
+      const int tiles = (n + most - 1) / most;
+      per = (n + tiles - 1) / tiles;
+    }
     return true;
   }
 };
 
-// One query tile: units [u0, u0 + nu) of the request, h0 of them in the first
-// half; nh columns per half.
+// One query tile: `nu` units from u on, h0 of them in the first half; nh
+// columns per half.
 struct Tile {
-  int u0, nu, h0, nh;
-  __device__ Tile(const Params& p, int units, int t) {
-    u0 = t * 2 * p.per_half;
-    nu = min(2 * p.per_half, units - u0);
+  int nu, h0, nh;
+  __device__ Tile(const Params& p, int u, int u1, int per) {
+    nu = min(per, u1 - u);
     h0 = (nu + 1) / 2;
     nh = (h0 * p.unit + 15) / 16 * 16;
   }
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sA = smem_u32(smem), sB = sA + (uint32_t)(p.slabs * kSlabBytes);
-  Shared& s = *reinterpret_cast<Shared*>(smem + (p.slabs + kStages) * kSlabBytes);
+  Shared& s = *reinterpret_cast<Shared*>(smem + p.slabs * kSlabBytes + kRingBytes);
   const uint32_t bar0 = smem_u32(s.bars);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarAFull + i), 1);
       mbar_init(bar(kBarAEmpty + i), 1);
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(bar(kBarBFull + i), 1);
       mbar_init(bar(kBarBEmpty + i), 1);
     }
@@ -228,12 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles += __shfl_sync(DDT_FULL_MASK, inc, 31);
     }
     longest = __reduce_max_sync(DDT_FULL_MASK, longest);
-    const int per = 2 * p.per_half, qt = (longest * p.chunks + per - 1) / per;
-    // lane S - 1 prices S shares: rounds of items times an item's query tiles
-    // plus about half a tile for its keys and its end
+    const int most = 2 * p.per_half, units = longest * p.chunks;
+    // lane S - 1 prices S shares: rounds of items times an item's columns (in
+    // units) plus about a third of a tile for its keys and its end
     const int S = lane + 1;
-    const bool may = S <= min(kMaxShares, max(qt, 1)) && (S == 1 || (long long)tiles * S <= kMaxParts);
-    const long long cost = may ? (((long long)tiles * S + npairs - 1) / npairs) * (2 * ((qt + S - 1) / S) + 1) : (1ll << 60);
+    const bool may = S <= min(kMaxShares, max(units, 1)) && (S == 1 || tiles <= kMaxParts / S);
+    const int rounds = may ? (tiles * S + npairs - 1) / npairs : 1;
+    const long long cost = may ? (long long)rounds * (3 * ((units + S - 1) / S) + (S > 1 ? 2 : 1) * most) : (1ll << 60);
     long long best = cost;
     int arg = S;
 #pragma unroll
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < p.nb; c += 32) {
       const int i = c + lane;
       int t = 0;
-      if (i < p.nb && s.len[i] > 0) t = (s.len[i] + 255) / 256 * max(1, min(arg, (s.m[i] * p.chunks + per - 1) / per));
+      if (i < p.nb && s.len[i] > 0) t = (s.len[i] + 255) / 256 * max(1, min(arg, s.m[i] * p.chunks));
       int inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -283,30 +296,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
     Cursor cur(pair);
-    int kt, share, nshare, t0, t1;
-    for (; ok && cur.get(s, p, kt, share, nshare, t0, t1); cur.item += npairs) {
-      if (t0 >= t1) continue;
-      const int b = p.b0 + cur.b, units = s.m[cur.b] * p.chunks;
+    int kt, share, nshare, u0, u1, per;
+    bool ahead = true;  // the first item's keys need no wait: all their loads go first
+    for (; ok && cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
+      if (u0 >= u1) continue;
+      const int b = p.b0 + cur.b;
       const int yk = (int)(w.cache_off[b] + kt * 256 + 128 * (int)rank);
       const int32_t* list = w.nodes ? w.nodes + (int64_t)b * w.M : nullptr;
-      for (int t = t0; t < t1 && ok; ++t) {
-        const Tile tile(p, units, t);
+      auto keys = [&](int k) {
+        if (leader) mbar_arrive_expect_tx(bar(kBarAFull + k), 2u * kSlabBytes);
+        tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, yk, afull0 + 8u * (uint32_t)k);
+      };
+      if (ahead && lane == 0)
+        for (int k = 0; k < p.slabs; ++k) keys(k);
+      for (int u = u0; u < u1 && ok; u += per) {
+        const Tile tile(p, u, u1, per);
         const bool mine = lane < (leader ? tile.h0 : tile.nu - tile.h0);
         int yq = 0;
         if (mine) {
-          const int u = tile.u0 + (leader ? 0 : tile.h0) + lane, e = u / p.chunks, c = u - e * p.chunks;
+          const int un = u + (leader ? 0 : tile.h0) + lane, e = un / p.chunks, c = un - e * p.chunks;
           yq = (b * w.N + (list ? __ldg(list + e) : e)) * w.H + c * p.unit;
         }
         const uint32_t dst = sB + (uint32_t)(lane * p.unit * 128);
         for (int k = 0; k < p.slabs; ++k) {
-          if (t == t0) {
+          if (u == u0 && !ahead) {
             if (!mbar_wait(bar(kBarAEmpty + k), aphase ^ 1u, abort, wlim)) ok = false;
             ok = __all_sync(DDT_FULL_MASK, ok);
             if (!ok) break;
-            if (lane == 0) {
-              if (leader) mbar_arrive_expect_tx(bar(kBarAFull + k), 2u * kSlabBytes);
-              tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, yk, afull0 + 8u * (uint32_t)k);
-            }
+            if (lane == 0) keys(k);
           }
           if (!mbar_wait(bar(kBarBEmpty + slot), phase ^ 1u, abort, wlim)) ok = false;
           ok = __all_sync(DDT_FULL_MASK, ok);
@@ -315,22 +332,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           ++issued;
           if (mine)
-            tma_load_2d_pair(dst + (uint32_t)(slot * kSlabBytes), &tm_q, 64 * k, yq, bfull0 + 8u * (uint32_t)slot);
-          if (++slot == kStages) {
+            tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes), &tm_q, 64 * k, yq, bfull0 + 8u * (uint32_t)slot);
+          if (++slot == p.stages) {
             slot = 0;
             phase ^= 1u;
           }
         }
       }
+      ahead = false;
       aphase ^= 1u;
     }
     if (!ok) {
       // a wait gave up: let the copies in flight land (bounded) before the
       // CTAs leave; the leader's barriers count both CTAs' bytes
       if (leader && lane == 0)
-        for (int i = 0; i < kStages && i < issued; ++i) {
+        for (int i = 0; i < p.stages && i < issued; ++i) {
           const int q = issued - 1 - i;
-          (void)mbar_wait_own(bar(kBarBFull + q % kStages), (uint32_t)((q / kStages) & 1), abort, wlim);
+          (void)mbar_wait_own(bar(kBarBFull + q % p.stages), (uint32_t)((q / p.stages) & 1), abort, wlim);
         }
       const uint64_t t = global_timer_ns();
       while (global_timer_ns() - t < 100000) __nanosleep(1000);
@@ -341,12 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
     Cursor cur(pair);
-    int kt, share, nshare, t0, t1;
-    for (; ok && cur.get(s, p, kt, share, nshare, t0, t1); cur.item += npairs) {
-      if (t0 >= t1) continue;
-      const int units = s.m[cur.b] * p.chunks;
-      for (int t = t0; t < t1 && ok; ++t, ++at) {
-        const Tile tile(p, units, t);
+    int kt, share, nshare, u0, u1, per;
+    for (; ok && cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
+      if (u0 >= u1) continue;
+      for (int u = u0; u < u1 && ok; u += per, ++at) {
+        const Tile tile(p, u, u1, per);
         const uint32_t idesc = idesc_bf16_f32(256, 2 * tile.nh, false, false);
         const int buf = at & 1;
         if (!mbar_wait(bar(kBarAccEmpty + buf), (uint32_t)((at >> 1) & 1) ^ 1u, abort, wlim)) {
@@ -356,19 +373,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * 256);
         for (int k = 0; k < p.slabs; ++k) {
-          if ((t == t0 && !mbar_wait(bar(kBarAFull + k), aphase, abort, wlim)) ||
+          if ((u == u0 && !mbar_wait(bar(kBarAFull + k), aphase, abort, wlim)) ||
               !mbar_wait(bar(kBarBFull + slot), phase, abort, wlim)) {
             ok = false;
             break;
           }
           const uint64_t da = smem_desc_sw128(sA + (uint32_t)(k * kSlabBytes), 16, 1024);
-          const uint64_t db = smem_desc_sw128(sB + (uint32_t)(slot * kSlabBytes), 16, 1024);
+          const uint64_t db = smem_desc_sw128(sB + (uint32_t)(slot * p.stage_bytes), 16, 1024);
           mma_pair_ss(d, da, db, idesc, k != 0 ? 1u : 0u);
 #pragma unroll
           for (int q = 1; q < 4; ++q) mma_pair_ss(d, da + 2 * q, db + 2 * q, idesc, 1u);
           mma_commit_pair_mc(bar(kBarBEmpty + slot), (uint16_t)0x3u);
-          if (t == t1 - 1) mma_commit_pair_mc(bar(kBarAEmpty + k), (uint16_t)0x3u);
-          if (++slot == kStages) {
+          if (u + per >= u1) mma_commit_pair_mc(bar(kBarAEmpty + k), (uint16_t)0x3u);
+          if (++slot == p.stages) {
             slot = 0;
             phase ^= 1u;
           }
@@ -389,20 +406,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     int at = 0;
     bool ok = true;
     Cursor cur(pair);
-    int kt, share, nshare, t0, t1;
-    for (; cur.get(s, p, kt, share, nshare, t0, t1); cur.item += npairs) {
-      const int b = p.b0 + cur.b, len = s.len[cur.b], m = s.m[cur.b], units = m * p.chunks;
+    int kt, share, nshare, u0, u1, per;
+    for (; cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
+      const int b = p.b0 + cur.b, len = s.len[cur.b], m = s.m[cur.b];
       const int32_t* list = w.nodes ? w.nodes + (int64_t)b * w.M : nullptr;
       const int key0 = kt * 256 + 128 * (int)rank, key = key0 + row, key1 = min(len, key0 + 128);
       // the log-sum-exp of column et of a tile and how many keys it sees (0:
       // no query row there, or one without visible keys)
-      auto column = [&](int t, float& l2, int& sees) {
-        const Tile tile(p, units, t);
+      auto column = [&](int u, float& l2, int& sees) {
+        const Tile tile(p, u, u1, per);
         const int half = et >= tile.nh ? 1 : 0, c = et - half * tile.nh, j = c / p.unit;
         l2 = 0.0f;
         sees = 0;
         if (et < 2 * tile.nh && j < (half ? tile.nu - tile.h0 : tile.h0)) {
-          const int u = tile.u0 + half * tile.h0 + j, e = u / p.chunks, head = (u - e * p.chunks) * p.unit + c - j * p.unit;
+          const int un = u + half * tile.h0 + j, e = un / p.chunks, head = (un - e * p.chunks) * p.unit + c - j * p.unit;
           if (head < w.H) {
             const int node = list ? __ldg(list + e) : e;
             const float l = __ldg(w.lse + ((long long)b * w.N + node) * w.H + head);
@@ -414,14 +431,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sum = 0.0f;
       float l2 = 0.0f;
       int sees = 0;
-      if (t0 < t1) column(t0, l2, sees);
-      for (int t = t0; t < t1; ++t, ++at) {
+      // what the end of the item needs, fetched under its tiles
+      const int64_t j = w.cache_off[b] + key;
+      const float old = w.prev && h == 0 && key < len ? w.prev[j] : 0.0f;
+      if (u0 < u1) column(u0, l2, sees);
+      for (int u = u0; u < u1; u += per, ++at) {
         const int buf = at & 1;
-        const Tile tile(p, units, t);
+        const Tile tile(p, u, u1, per);
         s.lse2[buf][et] = l2;
         s.sees[buf][et] = sees;
         const bool plain = bar_red_and(1, 256, et >= 2 * tile.nh || sees >= key1);
-        if (t + 1 < t1) column(t + 1, l2, sees);  // the next tile's, under this one
+        if (u + per < u1) column(u + per, l2, sees);  // the next tile's, under this one
         if (ok && !mbar_wait(bar(kBarAccFull + buf), (uint32_t)((at >> 1) & 1), abort, wlim)) ok = false;
         tc_fence_after();
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -467,29 +487,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 256);
       if (h == 0) {
         sum += s.half[row];
-        const int64_t j = w.cache_off[b] + key;
         bool write = ok;
         if (nshare > 1) {
           const int part = s.tile0[cur.b] + kt;
           float* mine = p.parts + ((int64_t)part * s.shares) * 256 + 128 * (int)rank + row;
           __stcg(mine + share * 256, sum);
-          __threadfence();
           named_bar_sync(2, 128);
           if (et == 0) {
+            // the barrier orders the CTA's partial sums before this thread's
+            // release; its acquire, and the next barrier, the others' before
+            // their reading
             unsigned* cnt = p.counters + 2 * part + rank;
-            const unsigned old = ok ? atomicAdd(cnt, 1u) : 0u;
-            s.last = ok && old == (unsigned)nshare - 1u;
+            unsigned old_count = 0u;
+            if (ok) asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(old_count) : "l"(cnt) : "memory");
+            s.last = ok && old_count == (unsigned)nshare - 1u;
             if (s.last) *cnt = 0u;
           }
           named_bar_sync(2, 128);
           write = ok && *reinterpret_cast<volatile int*>(&s.last) != 0;
           if (write) {
-            __threadfence();
             sum = 0.0f;
-            for (int i = 0; i < nshare; ++i) sum += __ldcg(mine + i * 256);
+#pragma unroll
+            for (int i = 0; i < kMaxShares; ++i) sum += i < nshare ? __ldcg(mine + i * 256) : 0.0f;
           }
         }
-        if (write && key < len) w.score[j] = w.prev ? fmaf(w.decay, w.prev[j], sum) : sum;
+        if (write && key < len) w.score[j] = w.prev ? fmaf(w.decay, old, sum) : sum;
       }
       named_bar_sync(1, 256);  // s.half is free again
     }
@@ -529,7 +551,7 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t d, uint64_t rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static size_t smem_bytes(int slabs) { return (size_t)(slabs + kStages) * kSlabBytes + sizeof(Shared) + 1024; }
+static size_t smem_bytes(int slabs) { return (size_t)slabs * kSlabBytes + kRingBytes + sizeof(Shared) + 1024; }
 
 // CTA pairs resident at once on the current device, looked up once per device
 // (with the shared-memory opt-in set).
@@ -593,6 +615,10 @@ int launch_cache_weights_tc(WeightsParams w, int max_cache_len, void* workspace,
     }
   }
   p.per_half = 128 / p.unit;
+  // stages as large as half a tile of this launch can be
+  const long long units = std::min(2LL * p.per_half, (long long)w.M * p.chunks);
+  p.stage_bytes = (int)(((units + 1) / 2 * p.unit + 15) / 16 * 16 * 128);
+  p.stages = std::min(kMaxStages, kRingBytes / p.stage_bytes);
   p.sl2 = w.scale * kLog2e;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.abort = reinterpret_cast<int*>(ws);
