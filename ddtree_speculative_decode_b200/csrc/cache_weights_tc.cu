@@ -18,8 +18,11 @@
 // more smaller ones when the tiles are small), fetched by
 // node from the caller's list: a unit is a node's heads or an even share of
 // them (padded to 8 rows, at most 128), which are consecutive rows of q.
-// Slabs are released one by one behind the item's last tile, so the next
-// item's keys arrive under its MMAs. Accumulators: two of 256 columns, so the
+// A commit costs the issuing thread about 300 cycles, so a stage has one: it
+// releases the stage's query rows and, in an item's last tile, the keys they
+// were multiplied with (two commits per 64 dims took 670 cycles, whatever the
+// tile's size); small tiles put three slabs into a stage. The next item's keys
+// arrive under this item's last MMAs. Accumulators: two of 256 columns, so the
 // exponentials of a tile run under the next tile's MMAs.
 //
 // Bound: the tensor pipe for 4 and more nodes of 64 heads (256 x 256 x 576
@@ -46,17 +49,18 @@ namespace cwt {
 using namespace sm100;
 
 constexpr int kThreads = 320;        // warp 0 TMA, warp 1 MMA + TMEM, warps 2..9 weights
-constexpr int kSlabBytes = 128 * 128;  // 128 rows x 64 dims bf16
 constexpr int kMaxSlabs = 9;
 constexpr int kMaxStages = 16;
-constexpr int kRingBytes = 4 * kSlabBytes;  // stages of query rows
+constexpr int kRingBytes = 64 * 1024;  // stages of query rows
+constexpr int kKeys = 128;             // keys of one CTA
+constexpr int kTile = 2 * kKeys;       // of the pair: M = 256
+constexpr int kSlabBytes = kKeys * 128;  // 128 keys x 64 dims bf16
 constexpr int kMaxB = 256;           // requests of one launch
 constexpr int kMaxShares = 16;
 constexpr int kMaxParts = 320;       // (key tile, share) partials of a split launch
 
-constexpr int kBarAFull = 0;                          // [kMaxSlabs] leader: a slab of keys (both CTAs)
-constexpr int kBarAEmpty = kBarAFull + kMaxSlabs;     // [kMaxSlabs] each CTA: the item's MMAs are done with it
-constexpr int kBarBFull = kBarAEmpty + kMaxSlabs;     // [kMaxStages] leader: a stage of query rows
+constexpr int kBarAFull = 0;                          // [kMaxSlabs] leader: a stage's keys (both CTAs)
+constexpr int kBarBFull = kBarAFull + kMaxSlabs;      // [kMaxStages] leader: a stage of query rows
 constexpr int kBarBEmpty = kBarBFull + kMaxStages;    // [kMaxStages] each CTA
 constexpr int kBarAccFull = kBarBEmpty + kMaxStages;     // [2] each CTA
 constexpr int kBarAccEmpty = kBarAccFull + 2;         // [2] leader: read by 8 warps x 2 CTAs
@@ -69,7 +73,8 @@ struct Shared {  // behind the slabs and stages
   int shares, total, last;
   alignas(16) float lse2[2][256];
   alignas(16) int sees[2][256];
-  float half[128];
+  float sums[2][kKeys];  // a key's parts
+  int64_t off[kMaxB];
   int len[kMaxB];        // -1: the request is skipped
   int m[kMaxB];          // entries of its list
   int tile0[kMaxB + 1];  // key tiles before it
@@ -83,6 +88,8 @@ struct Params {
   int unit;              // query rows of one unit (a multiple of 8, at most 128)
   int chunks;            // units per node
   int per_half;          // units that fit half a tile's 128 columns
+  int per_tile;          // stages of a tile
+  int row_bytes;         // of one slab of a stage's query rows
   int stages, stage_bytes;  // of the ring of query rows
   float sl2;             // scale log2 e
   int* abort;
@@ -90,6 +97,10 @@ struct Params {
   float* parts;          // [kMaxParts][256] partial sums
   uint64_t wait_ns;
 };
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ bool bar_red_and(int id, int nthreads, bool pred) {
   uint32_t r;
@@ -143,10 +154,12 @@ struct Tile {
   __device__ Tile(const Params& p, int u, int u1, int per) {
     nu = min(per, u1 - u);
     h0 = (nu + 1) / 2;
-    nh = (h0 * p.unit + 15) / 16 * 16;
+    nh = (h0 * p.unit + 31) / 32 * 32;
   }
 };
 
+// kKps: slabs of one stage
+template <int kKps>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, Params p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -166,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlabs; ++i) {
       mbar_init(bar(kBarAFull + i), 1);
-      mbar_init(bar(kBarAEmpty + i), 1);
     }
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(bar(kBarBFull + i), 1);
@@ -186,11 +198,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(smem_u32(&s.tmem), 512);
     tmem_relinquish_pair();
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
   // a workspace whose status word holds a timeout: no work (the leader's
-  // reading counts for the pair)
-  if (leader && threadIdx.x == 0) s.aborted = *reinterpret_cast<volatile int*>(abort);
+  // reading counts for the pair; it writes it into the other CTA once that
+  // one is known to run)
+  const int held = leader && threadIdx.x == 32 ? *reinterpret_cast<volatile int*>(abort) : 0;
 
   // ---- every request's rows and list: alike in every CTA
   for (int i = warp; i < p.nb; i += kThreads / 32) {
@@ -215,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       s.len[i] = oob || bad ? -1 : len;
       s.m[i] = oob || bad ? 0 : m;
+      s.off[i] = off;
       if (blockIdx.x == 0 && w.dev_status)
         w.dev_status[b] = *reinterpret_cast<volatile int*>(abort) != 0 ? DDT_ERR_TIMEOUT
                           : oob                                         ? DDT_ERR_BOUNDS
@@ -222,13 +238,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                         : DDT_OK;
     }
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (leader && threadIdx.x == 32) {
+    st_cluster_u32(map_to_rank(smem_u32(&s.aborted), 0), (uint32_t)held);
+    st_cluster_u32(map_to_rank(smem_u32(&s.aborted), 1), (uint32_t)held);
+  }
   __syncthreads();
   if (warp == 0) {
     // prefix of key tiles and the longest list, then the shares
     int tiles = 0, longest = 0;
     for (int c = 0; c < p.nb; c += 32) {
       const int i = c + lane;
-      const int t = i < p.nb && s.len[i] > 0 ? (s.len[i] + 255) / 256 : 0;
+      const int t = i < p.nb && s.len[i] > 0 ? (s.len[i] + kTile - 1) / kTile : 0;
       longest = max(longest, i < p.nb ? s.m[i] : 0);
       int inc = t;
 #pragma unroll
@@ -245,24 +267,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // units) plus about a third of a tile for its keys and its end
     const int S = lane + 1;
     const bool may = S <= min(kMaxShares, max(units, 1)) && (S == 1 || tiles <= kMaxParts / S);
-    const int rounds = may ? (tiles * S + npairs - 1) / npairs : 1;
-    const long long cost = may ? (long long)rounds * (3 * ((units + S - 1) / S) + (S > 1 ? 2 : 1) * most) : (1ll << 60);
-    long long best = cost;
-    int arg = S;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const long long c2 = __shfl_xor_sync(DDT_FULL_MASK, best, o);
-      const int a2 = __shfl_xor_sync(DDT_FULL_MASK, arg, o);
-      if (c2 < best || (c2 == best && a2 < arg)) {
-        best = c2;
-        arg = a2;
-      }
+    uint32_t cost = 0xffffffffu;
+    if (may && S > 1) {  // tiles * S is small
+      const int rounds = (tiles * S + npairs - 1) / npairs;
+      cost = (uint32_t)min((long long)rounds * (3 * ((units + S - 1) / S) + 2 * most), 0x7ffffffLL) << 5 | (uint32_t)lane;
+    } else if (may) {
+      cost = (uint32_t)min((long long)((tiles + npairs - 1) / npairs) * (3 * units + most), 0x7ffffffLL) << 5;
     }
+    const int arg = (int)(__reduce_min_sync(DDT_FULL_MASK, cost) & 31u) + 1;
     int items = 0;
     for (int c = 0; c < p.nb; c += 32) {
       const int i = c + lane;
       int t = 0;
-      if (i < p.nb && s.len[i] > 0) t = (s.len[i] + 255) / 256 * max(1, min(arg, s.m[i] * p.chunks));
+      if (i < p.nb && s.len[i] > 0) t = (s.len[i] + kTile - 1) / kTile * max(1, min(arg, s.m[i] * p.chunks));
       int inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -282,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
-  const bool aborted = ld_cluster_u32(map_to_rank(smem_u32(&s.aborted), 0)) != 0u;
+  const bool aborted = *reinterpret_cast<volatile int*>(&s.aborted) != 0;
 
   if (aborted) {
     // straight to the teardown
@@ -293,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // index arithmetic took 1400 cycles per stage, three times the MMAs' 512)
     const uint32_t afull0 = map_to_rank(bar(kBarAFull), 0), bfull0 = map_to_rank(bar(kBarBFull), 0);
     int slot = 0, issued = 0;
-    uint32_t phase = 0, aphase = 0;
+    uint32_t phase = 0;
     bool ok = true;
     Cursor cur(pair);
     int kt, share, nshare, u0, u1, per;
@@ -301,14 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
       if (u0 >= u1) continue;
       const int b = p.b0 + cur.b;
-      const int yk = (int)(w.cache_off[b] + kt * 256 + 128 * (int)rank);
+      const int yk = (int)(s.off[cur.b] + kt * kTile + kKeys * (int)rank);
       const int32_t* list = w.nodes ? w.nodes + (int64_t)b * w.M : nullptr;
-      auto keys = [&](int k) {
-        if (leader) mbar_arrive_expect_tx(bar(kBarAFull + k), 2u * kSlabBytes);
-        tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, yk, afull0 + 8u * (uint32_t)k);
+      auto keys = [&](int j) {  // the keys' slabs of stage j of a tile
+        const int k0 = j * kKps, k1 = min(p.slabs, k0 + kKps);
+        if (leader) mbar_arrive_expect_tx(bar(kBarAFull + j), 2u * kSlabBytes * (uint32_t)(k1 - k0));
+        for (int k = k0; k < k1; ++k)
+          tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, yk, afull0 + 8u * (uint32_t)j);
       };
       if (ahead && lane == 0)
-        for (int k = 0; k < p.slabs; ++k) keys(k);
+        for (int j = 0; j < p.per_tile; ++j) keys(j);
       for (int u = u0; u < u1 && ok; u += per) {
         const Tile tile(p, u, u1, per);
         const bool mine = lane < (leader ? tile.h0 : tile.nu - tile.h0);
@@ -318,21 +337,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           yq = (b * w.N + (list ? __ldg(list + e) : e)) * w.H + c * p.unit;
         }
         const uint32_t dst = sB + (uint32_t)(lane * p.unit * 128);
-        for (int k = 0; k < p.slabs; ++k) {
+        for (int j = 0; j < p.per_tile; ++j) {
           if (u == u0 && !ahead) {
-            if (!mbar_wait(bar(kBarAEmpty + k), aphase ^ 1u, abort, wlim)) ok = false;
-            ok = __all_sync(DDT_FULL_MASK, ok);
-            if (!ok) break;
-            if (lane == 0) keys(k);
+            // the keys of this stage are free when the last tile's stage j is
+            // done with: known already if its slot has been filled again
+            const int g = issued - p.per_tile;  // that stage's number
+            if (g + p.stages >= issued) {
+              if (!mbar_wait(bar(kBarBEmpty + g % p.stages), (uint32_t)((g / p.stages) & 1), abort, wlim)) ok = false;
+              ok = __all_sync(DDT_FULL_MASK, ok);
+              if (!ok) break;
+            }
+            if (lane == 0) keys(j);
           }
           if (!mbar_wait(bar(kBarBEmpty + slot), phase ^ 1u, abort, wlim)) ok = false;
           ok = __all_sync(DDT_FULL_MASK, ok);
           if (!ok) break;
-          if (leader && lane == 0) mbar_arrive_expect_tx(bar(kBarBFull + slot), (uint32_t)(tile.nu * p.unit * 128));
+          const int k0 = j * kKps, n = kKps == 1 ? 1 : min(p.slabs - k0, kKps);
+          if (leader && lane == 0)
+            mbar_arrive_expect_tx(bar(kBarBFull + slot), (uint32_t)(n * tile.nu * p.unit * 128));
           __syncwarp();
           ++issued;
           if (mine)
-            tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes), &tm_q, 64 * k, yq, bfull0 + 8u * (uint32_t)slot);
+#pragma unroll
+            for (int i = 0; i < kKps; ++i)
+              if (i < n)
+                tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes + i * p.row_bytes), &tm_q, 64 * (k0 + i), yq,
+                                 bfull0 + 8u * (uint32_t)slot);
           if (++slot == p.stages) {
             slot = 0;
             phase ^= 1u;
@@ -340,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ahead = false;
-      aphase ^= 1u;
     }
     if (!ok) {
       // a wait gave up: let the copies in flight land (bounded) before the
@@ -364,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u0 >= u1) continue;
       for (int u = u0; u < u1 && ok; u += per, ++at) {
         const Tile tile(p, u, u1, per);
-        const uint32_t idesc = idesc_bf16_f32(256, 2 * tile.nh, false, false);
+        const uint32_t idesc = idesc_bf16_f32(kTile, 2 * tile.nh, false, false);
         const int buf = at & 1;
         if (!mbar_wait(bar(kBarAccEmpty + buf), (uint32_t)((at >> 1) & 1) ^ 1u, abort, wlim)) {
           ok = false;
@@ -372,19 +401,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * 256);
-        for (int k = 0; k < p.slabs; ++k) {
-          if ((u == u0 && !mbar_wait(bar(kBarAFull + k), aphase, abort, wlim)) ||
+        for (int j = 0; j < p.per_tile; ++j) {
+          if ((u == u0 && !mbar_wait(bar(kBarAFull + j), aphase, abort, wlim)) ||
               !mbar_wait(bar(kBarBFull + slot), phase, abort, wlim)) {
             ok = false;
             break;
           }
-          const uint64_t da = smem_desc_sw128(sA + (uint32_t)(k * kSlabBytes), 16, 1024);
-          const uint64_t db = smem_desc_sw128(sB + (uint32_t)(slot * p.stage_bytes), 16, 1024);
-          mma_pair_ss(d, da, db, idesc, k != 0 ? 1u : 0u);
+          const int k0 = j * kKps, n = kKps == 1 ? 1 : min(p.slabs - k0, kKps);
 #pragma unroll
-          for (int q = 1; q < 4; ++q) mma_pair_ss(d, da + 2 * q, db + 2 * q, idesc, 1u);
+          for (int i = 0; i < kKps; ++i) {
+            if (i < n) {
+              const uint64_t da = smem_desc_sw128(sA + (uint32_t)((k0 + i) * kSlabBytes), 16, 1024);
+              const uint64_t db = smem_desc_sw128(sB + (uint32_t)(slot * p.stage_bytes + i * p.row_bytes), 16, 1024);
+              mma_pair_ss(d, da, db, idesc, (j | i) != 0 ? 1u : 0u);
+#pragma unroll
+              for (int q = 1; q < 4; ++q) mma_pair_ss(d, da + 2 * q, db + 2 * q, idesc, 1u);
+            }
+          }
           mma_commit_pair_mc(bar(kBarBEmpty + slot), (uint16_t)0x3u);
-          if (u + per >= u1) mma_commit_pair_mc(bar(kBarAEmpty + k), (uint16_t)0x3u);
           if (++slot == p.stages) {
             slot = 0;
             phase ^= 1u;
@@ -396,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 2) {
     // ============================================================ weights
-    // thread = lane 32 q + lane of the CTA's tensor memory = key 128 rank +
-    // 32 q + lane of the tile; half h of the quarter's two warps takes the
-    // 32-column chunks h, h + 2, ...
+    // thread = lane 32 q + lane of the CTA's tensor memory = that key of the
+    // CTA; of the two warps per lane quarter each takes every other chunk of 32
+    // columns
     const int q = warp & 3, h = warp >= 6 ? 1 : 0, et = (int)threadIdx.x - 64;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t empty0 = map_to_rank(bar(kBarAccEmpty), 0);
@@ -410,15 +444,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
       const int b = p.b0 + cur.b, len = s.len[cur.b], m = s.m[cur.b];
       const int32_t* list = w.nodes ? w.nodes + (int64_t)b * w.M : nullptr;
-      const int key0 = kt * 256 + 128 * (int)rank, key = key0 + row, key1 = min(len, key0 + 128);
+      const int key0 = kt * kTile + kKeys * (int)rank, key = key0 + row, key1 = min(len, key0 + kKeys);
       // the log-sum-exp of column et of a tile and how many keys it sees (0:
       // no query row there, or one without visible keys)
       auto column = [&](int u, float& l2, int& sees) {
         const Tile tile(p, u, u1, per);
-        const int half = et >= tile.nh ? 1 : 0, c = et - half * tile.nh, j = c / p.unit;
+        const int half = et >> 7, c = et & 127, j = c / p.unit;
         l2 = 0.0f;
         sees = 0;
-        if (et < 2 * tile.nh && j < (half ? tile.nu - tile.h0 : tile.h0)) {
+        if (c < tile.nh && j < (half ? tile.nu - tile.h0 : tile.h0)) {
           const int un = u + half * tile.h0 + j, e = un / p.chunks, head = (un - e * p.chunks) * p.unit + c - j * p.unit;
           if (head < w.H) {
             const int node = list ? __ldg(list + e) : e;
@@ -432,15 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l2 = 0.0f;
       int sees = 0;
       // what the end of the item needs, fetched under its tiles
-      const int64_t j = w.cache_off[b] + key;
-      const float old = w.prev && h == 0 && key < len ? w.prev[j] : 0.0f;
+      const int64_t j = s.off[cur.b] + key0 + et;
+      const float old = w.prev && et < kKeys && key0 + et < len ? w.prev[j] : 0.0f;
       if (u0 < u1) column(u0, l2, sees);
       for (int u = u0; u < u1; u += per, ++at) {
         const int buf = at & 1;
         const Tile tile(p, u, u1, per);
         s.lse2[buf][et] = l2;
         s.sees[buf][et] = sees;
-        const bool plain = bar_red_and(1, 256, et >= 2 * tile.nh || sees >= key1);
+        const bool plain = bar_red_and(1, 256, (et & 127) >= tile.nh || sees >= key1);
         if (u + per < u1) column(u + per, l2, sees);  // the next tile's, under this one
         if (ok && !mbar_wait(bar(kBarAccFull + buf), (uint32_t)((at >> 1) & 1), abort, wlim)) ok = false;
         tc_fence_after();
@@ -451,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[32];
           tmem_ld32(lane_addr + (uint32_t)(buf * 256 + 32 * c), r);
           tmem_wait_ld();
-          const float4* pl = reinterpret_cast<const float4*>(&s.lse2[buf][32 * c]);
+          const int col = 32 * c >= tile.nh ? 128 + 32 * c - tile.nh : 32 * c;  // of lse2 and sees
+          const float4* pl = reinterpret_cast<const float4*>(&s.lse2[buf][col]);
           if (plain) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -462,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[3] += ex2_ftz(fmaf(__uint_as_float(r[4 * i + 3]), p.sl2, -l.w));
             }
           } else {
-            const int4* ps = reinterpret_cast<const int4*>(&s.sees[buf][32 * c]);
+            const int4* ps = reinterpret_cast<const int4*>(&s.sees[buf][col]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 l = pl[i];
@@ -482,17 +517,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);  // tile by tile: short chains of additions
       }
-      // ---- the key's two halves, then the shares
-      if (h == 1) s.half[row] = sum;
+      // ---- the key's parts, then the shares
+      s.sums[h][row] = sum;
       named_bar_sync(1, 256);
-      if (h == 0) {
-        sum += s.half[row];
+      if (et < kKeys) {  // whose row is et: key0 + et
+        const int key = key0 + et;
+        sum = s.sums[0][et] + s.sums[1][et];
         bool write = ok;
         if (nshare > 1) {
           const int part = s.tile0[cur.b] + kt;
-          float* mine = p.parts + ((int64_t)part * s.shares) * 256 + 128 * (int)rank + row;
-          __stcg(mine + share * 256, sum);
-          named_bar_sync(2, 128);
+          float* mine = p.parts + ((int64_t)part * s.shares) * kTile + kKeys * (int)rank + et;
+          __stcg(mine + share * kTile, sum);
+          named_bar_sync(2, kKeys);
           if (et == 0) {
             // the barrier orders the CTA's partial sums before this thread's
             // release; its acquire, and the next barrier, the others' before
@@ -503,17 +539,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.last = ok && old_count == (unsigned)nshare - 1u;
             if (s.last) *cnt = 0u;
           }
-          named_bar_sync(2, 128);
+          named_bar_sync(2, kKeys);
           write = ok && *reinterpret_cast<volatile int*>(&s.last) != 0;
           if (write) {
             sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kMaxShares; ++i) sum += i < nshare ? __ldcg(mine + i * 256) : 0.0f;
+            for (int i = 0; i < kMaxShares; ++i) sum += i < nshare ? __ldcg(mine + i * kTile) : 0.0f;
           }
         }
         if (write && key < len) w.score[j] = w.prev ? fmaf(w.decay, old, sum) : sum;
       }
-      named_bar_sync(1, 256);  // s.half is free again
+      named_bar_sync(1, 256);  // s.sums is free again
     }
   }
   // ---------------------------------------------------------------- teardown
@@ -551,10 +587,13 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t d, uint64_t rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static size_t smem_bytes(int slabs) { return (size_t)slabs * kSlabBytes + kRingBytes + sizeof(Shared) + 1024; }
+static size_t smem_bytes(int slabs) {
+  return (size_t)slabs * kSlabBytes + kRingBytes + sizeof(Shared) + 1024;
+}
 
 // CTA pairs resident at once on the current device, looked up once per device
 // (with the shared-memory opt-in set).
+template <int kKps>
 static int device_pairs() {
   static std::mutex mu;
   static int pairs[kMaxDevices] = {0};
@@ -562,7 +601,7 @@ static int device_pairs() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
   std::lock_guard<std::mutex> lock(mu);
   if (pairs[dev] == 0) {
-    if (cudaFuncSetAttribute(cache_weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(cache_weights_tc_kernel<kKps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem_bytes(kMaxSlabs)) != cudaSuccess)
       return -1;
     cudaLaunchConfig_t cfg = {};
@@ -577,7 +616,7 @@ static int device_pairs() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, cache_weights_tc_kernel, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, cache_weights_tc_kernel<kKps>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
       n = sm_count() / 2;
     }
@@ -594,6 +633,42 @@ bool weights_tc_supported(int d_qk, int in_dtype, const void* q, const void* kv)
 }
 
 size_t weights_tc_workspace_bytes() { return 256 + cwt::kMaxParts * 2 * sizeof(unsigned) + cwt::kMaxParts * 256 * sizeof(float); }
+
+namespace cwt {
+template <int kKps>
+static int launch(Params p, int max_cache_len, cudaStream_t stream) {
+  const WeightsParams& w = p.w;
+  const int pairs = device_pairs<kKps>();
+  if (pairs <= 0) return DDT_ERR_CUDA;
+  CUtensorMap tk, tq;
+  if (!make_map(&tk, w.kv, (uint64_t)w.d_qk, (uint64_t)w.kv_rows, kKeys) ||
+      !make_map(&tq, w.q, (uint64_t)w.d_qk, (uint64_t)w.B * w.N * w.H, (uint32_t)p.unit))
+    return DDT_ERR_CUDA;
+  for (p.b0 = 0; p.b0 < w.B; p.b0 += kMaxB) {
+    p.nb = std::min(kMaxB, w.B - p.b0);
+    // every pair that could get an item, counting shares
+    const long long tiles = std::max(1LL, (long long)p.nb * ((max_cache_len + kTile - 1) / kTile));
+    const long long items = tiles * std::min<long long>(kMaxShares, std::max(1LL, (long long)w.M * p.chunks));
+    const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, items);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(p.slabs);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, cache_weights_tc_kernel<kKps>, tk, tq, p) != cudaSuccess) return DDT_ERR_CUDA;
+  }
+  return DDT_OK;
+}
+}  // namespace cwt
 
 int launch_cache_weights_tc(WeightsParams w, int max_cache_len, void* workspace, cudaStream_t stream) {
   using namespace cwt;
@@ -617,7 +692,10 @@ int launch_cache_weights_tc(WeightsParams w, int max_cache_len, void* workspace,
   p.per_half = 128 / p.unit;
   // stages as large as half a tile of this launch can be
   const long long units = std::min(2LL * p.per_half, (long long)w.M * p.chunks);
-  p.stage_bytes = (int)(((units + 1) / 2 * p.unit + 15) / 16 * 16 * 128);
+  p.row_bytes = (int)(((units + 1) / 2 * p.unit + 31) / 32 * 32 * 128);
+  const int kps = 3 * p.row_bytes <= kRingBytes / 4 ? 3 : 1;
+  p.per_tile = (p.slabs + kps - 1) / kps;
+  p.stage_bytes = kps * p.row_bytes;
   p.stages = std::min(kMaxStages, kRingBytes / p.stage_bytes);
   p.sl2 = w.scale * kLog2e;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -625,35 +703,7 @@ int launch_cache_weights_tc(WeightsParams w, int max_cache_len, void* workspace,
   p.counters = reinterpret_cast<unsigned*>(ws + 256);
   p.parts = reinterpret_cast<float*>(ws + 256 + kMaxParts * 2 * sizeof(unsigned));
   p.wait_ns = wait_limit_ns();
-  const int pairs = device_pairs();
-  if (pairs <= 0) return DDT_ERR_CUDA;
-  CUtensorMap tk, tq;
-  if (!make_map(&tk, w.kv, (uint64_t)w.d_qk, (uint64_t)w.kv_rows, 128) ||
-      !make_map(&tq, w.q, (uint64_t)w.d_qk, (uint64_t)w.B * w.N * w.H, (uint32_t)p.unit))
-    return DDT_ERR_CUDA;
-  for (p.b0 = 0; p.b0 < w.B; p.b0 += kMaxB) {
-    p.nb = std::min(kMaxB, w.B - p.b0);
-    // every pair that could get an item, counting shares
-    const long long tiles = std::max(1LL, (long long)p.nb * ((max_cache_len + 255) / 256));
-    const long long items = tiles * std::min<long long>(kMaxShares, std::max(1LL, (long long)w.M * p.chunks));
-    const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, items);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(p.slabs);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, cache_weights_tc_kernel, tk, tq, p) != cudaSuccess) return DDT_ERR_CUDA;
-  }
-  return DDT_OK;
+  return kps == 3 ? launch<3>(p, max_cache_len, stream) : launch<1>(p, max_cache_len, stream);
 }
 
 }  // namespace ddt
