@@ -62,7 +62,7 @@ constexpr int kRound = kU * kThreads;
 constexpr int kStages = 3;        // rounds of the ring
 constexpr int kRingBytes = kStages * kRound * 16;
 constexpr int kMaxC = 8;          // CTAs that may share a row
-constexpr int kListMax = 1024;    // entries of a launch that follows a node list
+constexpr int kOwn = 256;         // rows of one CTA in a launch that follows a node list
 constexpr int kStep = 64;         // threads that add keys between two looks in the careful pass
 constexpr int kBest = 4;          // warps whose published values make the bound
 constexpr int kWarpCand = 96;     // keys of a warp's buffer
@@ -366,8 +366,8 @@ __device__ __forceinline__ uint32_t nth_largest(const uint32_t* values, int r, i
 template <bool kBF16, bool kTop>
 __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsParams p) {
   extern __shared__ __align__(16) unsigned char s_ring[];  // [kStages][kU][kThreads] vectors
-  __shared__ uint16_t s_list[kListMax];
-  __shared__ int s_row[kListMax];  // the entry's logits row, -1: no such node
+  __shared__ int s_list[kOwn];  // this CTA's entries of a node list
+  __shared__ int s_row[kOwn];   // and their logits rows, -1: no such node
   __shared__ int s_wcount[kWarps];
   __shared__ Sums s_sums[2][kWarps];
   __shared__ __align__(16) Part s_part[2][kMaxC];
@@ -388,32 +388,18 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   pdl_launch_dependents();
 
   // ---- the selected entries: all of them, or those of the list whose node is
-  // not negative; the others are written as skipped by the CTAs in turn
-  int live = p.R;
+  // not negative, counted by warps over their eighths of it; the others are
+  // written as skipped by the CTAs in turn
+  int live = p.R, before = 0;
+  const int eighth = (p.R + 32 * kWarps - 1) / (32 * kWarps) * 32, e0 = warp * eighth, e1 = min(p.R, e0 + eighth);
   if (p.nodes) {
-    int base = 0;
-    for (int c0 = 0; c0 < p.R; c0 += kThreads) {
-      const int e = c0 + tid;
+#pragma unroll 4
+    for (int e = e0 + lane; e < e1 + lane; e += 32) {
+      const bool in = e < e1;
       const long long o = p.e0 + e;
-      const int node = e < p.R ? __ldg(p.nodes + o) : -1;
-      const bool on = node >= 0;
-      const unsigned votes = __ballot_sync(DDT_FULL_MASK, on);
-      if (lane == 0) s_wcount[warp] = __popc(votes);
-      __syncthreads();
-      int at = base + __popc(votes & ((1u << lane) - 1u));
-      int all = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const int n = s_wcount[w];
-        at += w < warp ? n : 0;
-        all += n;
-      }
-      base += all;
-      if (on) {
-        s_list[at] = (uint16_t)e;
-        s_row[at] = node < p.N ? (int)(o / p.M) * p.N + node : -1;
-      }
-      if (!on && e < p.R && e % (int)gridDim.x == (int)blockIdx.x) {
+      const bool on = in && __ldg(p.nodes + o) >= 0;
+      before += __popc(__ballot_sync(DDT_FULL_MASK, on));
+      if (in && !on && (unsigned)e % gridDim.x == blockIdx.x) {
         p.logp[o] = 0.0f;
         if (p.entropy) p.entropy[o] = 0.0f;
         for (int k = 0; k < K; ++k) {
@@ -422,9 +408,12 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         }
         if (p.dev_status) p.dev_status[o] = DDT_OK;
       }
-      __syncthreads();
     }
-    live = base;
+    if (lane == 0) s_wcount[warp] = before;
+    __syncthreads();
+    const int n = lane < kWarps ? s_wcount[lane] : 0;
+    live = __reduce_add_sync(DDT_FULL_MASK, n);
+    before = __reduce_add_sync(DDT_FULL_MASK, lane < warp ? n : 0);
   }
   if (live == 0) return;  // the same on every CTA
 
@@ -437,11 +426,11 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   if (lc < 0) {
     lc = 0;
     const int fixed = kTop ? 1500 : 500;
-    long long best = -1;
+    float best = 0.0f;
     for (int l = 0; rest > 0 && (1 << l) <= csize; ++l) {
-      const int g = grid >> l;
-      const long long cost = (long long)((rest + g - 1) / g) * ((V / kPer >> l) + fixed);
-      if (best < 0 || cost < best) {
+      const unsigned g = (unsigned)grid >> l;
+      const float cost = (float)(((unsigned)rest + g - 1u) / g) * (float)((V / kPer >> l) + fixed);
+      if (l == 0 || cost < best) {
         best = cost;
         lc = l;
       }
@@ -452,6 +441,25 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   const int group = (int)blockIdx.x >> lc, part = (int)blockIdx.x & (C - 1);
   const int lead = crank - part;  // the group's first CTA, as a rank of the cluster
   const int rows = waves + (rest + groups - 1) / groups;  // of every CTA, some of the last ones empty
+  if (p.nodes) {  // this CTA's share of the selected entries, in order
+#pragma unroll 4
+    for (int e = e0 + lane; e < e1 + lane; e += 32) {
+      const long long o = p.e0 + e;
+      const int node = e < e1 ? __ldg(p.nodes + o) : -1;
+      const unsigned votes = __ballot_sync(DDT_FULL_MASK, node >= 0);
+      const int ord = before + __popc(votes & ((1u << lane) - 1u));
+      before += __popc(votes);
+      if (node < 0) continue;
+      const bool full = ord < waves * grid;
+      const unsigned d = full ? (unsigned)grid : (unsigned)groups, x = full ? (unsigned)ord : (unsigned)(ord - waves * grid);
+      const unsigned turn = x / d;
+      if (x - turn * d != (full ? blockIdx.x : (unsigned)group)) continue;
+      const int it = (full ? 0 : waves) + (int)turn;
+      s_list[it] = e;
+      s_row[it] = node < p.N ? (int)((unsigned)o / (unsigned)p.M) * p.N + node : -1;
+    }
+    __syncthreads();
+  }
   if (C > 1) cluster_sync();      // every CTA of the cluster runs before its shared memory is written
 
   // the it-th row of this CTA: its entry (-1: none), its logits (null: none)
@@ -463,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     if (it >= rows || ord >= live) return;
     long long r;
     if (p.nodes) {
-      entry = p.e0 + s_list[ord];
-      r = s_row[ord];
+      entry = p.e0 + s_list[it];
+      r = s_row[it];
     } else {
       entry = ord;
       const unsigned b = (unsigned)ord / (unsigned)p.M;
@@ -978,12 +986,12 @@ static int launch_t(LogprobsParams p, cudaStream_t stream) {
     }
     if (slots == 0) slots = 3 * sm_count();
   };
-  // A node list selects few rows as a rule: clusters of 8, the split decided
-  // on the device. All rows: clusters of 4 (they leave fewer SMs unused) and
+  // A node list selects few rows as a rule: clusters of 8 (a long list: of 4),
+  // the split decided on the device. All rows: clusters of 4 (they leave fewer SMs unused) and
   // full waves if the rows fill the device; fewer rows are split so that one
   // wave of CTAs lies evenly on the SMs. One CTA alone keeps an SM about 45 %
   // busy, two 80 %.
-  int cluster = p.nodes ? kMaxC : 4;
+  int cluster = p.nodes && all <= 2048 ? kMaxC : 4;
   fit(cluster);
   p.log_share = -1;
   if (!p.nodes && all < slots) {
@@ -1011,11 +1019,16 @@ static int launch_t(LogprobsParams p, cudaStream_t stream) {
   p.cluster = cluster;
   const long long most = std::max(1, slots / cluster);
   const long long total = (long long)p.B * p.M;
-  const long long step = p.nodes ? kListMax : total;
+  const long long ctas = most * cluster;
+  const long long step = p.nodes ? std::min(1LL << 20, ctas * (kOwn / 2)) : total;
   for (long long e0 = 0; e0 < total; e0 += step) {
     p.e0 = e0;
     p.R = (int)std::min(step, total - e0);
-    const int grid = (int)(std::min<long long>(most, p.R) * cluster);
+    // A short list (a path among a tree's nodes) gets one CTA per SM rather
+    // than three, which leaves room for the next kernel to start under this
+    // one (8 rows of a list of 64: 7.2 against 9.0 us).
+    const long long clusters = p.nodes ? std::max<long long>(p.R / 4, sm_count() / cluster) : p.R;
+    const int grid = (int)(std::min({most, clusters, (long long)p.R}) * cluster);
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = config<kBF16, kTop>(attr, grid, cluster, stream);
     if (cudaLaunchKernelEx(&cfg, token_logprobs_kernel<kBF16, kTop>, p) != cudaSuccess) return DDT_ERR_CUDA;

@@ -129,6 +129,7 @@ def set_wait_limit_ns(ns: int) -> int:
 # objects, and the current stream's handle without a Stream object (3 us less
 # per call than torch.cuda.current_stream()).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # of an initialised runtime
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -139,11 +140,14 @@ def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_cur_device())
     return torch.cuda.current_stream().cuda_stream
 
 
 def _check(t: torch.Tensor, name: str, dtype, shape=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+            (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     if not t.is_cuda:
@@ -164,9 +168,14 @@ def _device(*tensors, stream=None):
     on (and the explicit stream, if any, belongs to) current for the launch;
     nothing is switched when it is current already (as inside a graph
     capture on that device)."""
-    idx = {t.get_device() for t in tensors if t is not None}  # -1 off the GPU
-    if len(idx) == 1 and stream is None and -1 not in idx and torch.cuda.current_device() in idx:
-        return _SAME_DEVICE
+    if stream is None:
+        first = tensors[0].get_device()  # -1 off the GPU
+        for t in tensors:
+            if t is not None and t.get_device() != first:
+                break
+        else:
+            if first >= 0 and _cur_device() == first:
+                return _SAME_DEVICE
     devs = {t.device for t in tensors if t is not None}
     if len(devs) != 1:
         raise ValueError(f"tensors of one call must share a CUDA device, got {sorted(map(str, devs))}")

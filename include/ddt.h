@@ -433,7 +433,7 @@ DDT_API int ddt_accept_compact_noalloc(const void* logits, int logits_dtype, int
  * Sizes: B, N, M, V >= 1, 0 <= K <= min(V, 32), M <= N when nodes is null;
  *   B * M and B * N < 2^31 and V <= 2^30 (DDT_ERR_UNSUPPORTED beyond).
  * Every selected row is read once; rows that no entry selects are not read.
- *   One launch (one per 1024 entries when nodes is given); no workspace.
+ *   One launch (several for a node list of tens of thousands of entries); no workspace.
  *   Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, alignment),
  *   DDT_ERR_UNSUPPORTED, DDT_ERR_CUDA (launch).
  */
