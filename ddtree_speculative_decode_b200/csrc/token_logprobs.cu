@@ -388,26 +388,40 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   pdl_launch_dependents();
 
   // ---- the selected entries: all of them, or those of the list whose node is
-  // not negative, counted by warps over their eighths of it; the others are
-  // written as skipped by the CTAs in turn
+  // not negative, counted by warps over their eighths of it, four neighbouring
+  // entries per lane (every CTA reads the whole list, so a list of 16384
+  // entries must not cost it more than a few hundred instructions per warp)
   int live = p.R, before = 0;
-  const int eighth = (p.R + 32 * kWarps - 1) / (32 * kWarps) * 32, e0 = warp * eighth, e1 = min(p.R, e0 + eighth);
+  const int eighth = (p.R + 128 * kWarps - 1) / (128 * kWarps) * 128, e0 = warp * eighth, e1 = min(p.R, e0 + eighth);
+  const int32_t* list = p.nodes ? p.nodes + p.e0 : nullptr;
+  auto four = [&](int e) {  // entries e .. e + 3, -1 behind the end
+    int4 x = make_int4(-1, -1, -1, -1);
+    if (e + 3 < e1 && reinterpret_cast<uintptr_t>(list) % 16 == 0) return __ldg(reinterpret_cast<const int4*>(list + e));
+    if (e < e1) x.x = __ldg(list + e);
+    if (e + 1 < e1) x.y = __ldg(list + e + 1);
+    if (e + 2 < e1) x.z = __ldg(list + e + 2);
+    if (e + 3 < e1) x.w = __ldg(list + e + 3);
+    return x;
+  };
   if (p.nodes) {
 #pragma unroll 4
-    for (int e = e0 + lane; e < e1 + lane; e += 32) {
-      const bool in = e < e1;
+    for (int e = e0 + 4 * lane; e < e1; e += 128) {
+      const int4 x = four(e);
+      before += (x.x >= 0 ? 1 : 0) + (x.y >= 0 ? 1 : 0) + (x.z >= 0 ? 1 : 0) + (x.w >= 0 ? 1 : 0);
+    }
+    before = __reduce_add_sync(DDT_FULL_MASK, before);
+    // skipped entries: each CTA writes those of its share of the list
+    const int share = (p.R + (int)gridDim.x - 1) / (int)gridDim.x, s0 = (int)blockIdx.x * share;
+    for (int e = s0 + tid; e < min(p.R, s0 + share); e += kThreads) {
+      if (__ldg(list + e) >= 0) continue;
       const long long o = p.e0 + e;
-      const bool on = in && __ldg(p.nodes + o) >= 0;
-      before += __popc(__ballot_sync(DDT_FULL_MASK, on));
-      if (in && !on && (unsigned)e % gridDim.x == blockIdx.x) {
-        p.logp[o] = 0.0f;
-        if (p.entropy) p.entropy[o] = 0.0f;
-        for (int k = 0; k < K; ++k) {
-          p.top_logp[o * K + k] = -INFINITY;
-          p.top_tok[o * K + k] = -1;
-        }
-        if (p.dev_status) p.dev_status[o] = DDT_OK;
+      p.logp[o] = 0.0f;
+      if (p.entropy) p.entropy[o] = 0.0f;
+      for (int k = 0; k < K; ++k) {
+        p.top_logp[o * K + k] = -INFINITY;
+        p.top_tok[o * K + k] = -1;
       }
+      if (p.dev_status) p.dev_status[o] = DDT_OK;
     }
     if (lane == 0) s_wcount[warp] = before;
     __syncthreads();
@@ -442,21 +456,29 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   const int lead = crank - part;  // the group's first CTA, as a rank of the cluster
   const int rows = waves + (rest + groups - 1) / groups;  // of every CTA, some of the last ones empty
   if (p.nodes) {  // this CTA's share of the selected entries, in order
-#pragma unroll 4
-    for (int e = e0 + lane; e < e1 + lane; e += 32) {
-      const long long o = p.e0 + e;
-      const int node = e < e1 ? __ldg(p.nodes + o) : -1;
-      const unsigned votes = __ballot_sync(DDT_FULL_MASK, node >= 0);
-      const int ord = before + __popc(votes & ((1u << lane) - 1u));
-      before += __popc(votes);
-      if (node < 0) continue;
+    auto mine = [&](int e, int node, int ord) {
       const bool full = ord < waves * grid;
       const unsigned d = full ? (unsigned)grid : (unsigned)groups, x = full ? (unsigned)ord : (unsigned)(ord - waves * grid);
       const unsigned turn = x / d;
-      if (x - turn * d != (full ? blockIdx.x : (unsigned)group)) continue;
+      if (x - turn * d != (full ? blockIdx.x : (unsigned)group)) return;
       const int it = (full ? 0 : waves) + (int)turn;
       s_list[it] = e;
-      s_row[it] = node < p.N ? (int)((unsigned)o / (unsigned)p.M) * p.N + node : -1;
+      s_row[it] = node < p.N ? (int)((unsigned)(p.e0 + e) / (unsigned)p.M) * p.N + node : -1;
+    };
+    const unsigned lower = (1u << lane) - 1u;
+#pragma unroll 2
+    for (int c = e0; c < e1; c += 128) {
+      const int e = c + 4 * lane;
+      const int4 x = four(e);
+      const unsigned v0 = __ballot_sync(DDT_FULL_MASK, x.x >= 0), v1 = __ballot_sync(DDT_FULL_MASK, x.y >= 0);
+      const unsigned v2 = __ballot_sync(DDT_FULL_MASK, x.z >= 0), v3 = __ballot_sync(DDT_FULL_MASK, x.w >= 0);
+      if ((v0 | v1 | v2 | v3) == 0u) continue;
+      int ord = before + __popc(v0 & lower) + __popc(v1 & lower) + __popc(v2 & lower) + __popc(v3 & lower);
+      before += __popc(v0) + __popc(v1) + __popc(v2) + __popc(v3);
+      if (x.x >= 0) mine(e, x.x, ord++);
+      if (x.y >= 0) mine(e + 1, x.y, ord++);
+      if (x.z >= 0) mine(e + 2, x.z, ord++);
+      if (x.w >= 0) mine(e + 3, x.w, ord);
     }
     __syncthreads();
   }
