@@ -374,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   __shared__ unsigned long long s_cand[kTop ? kCand : 1];
   __shared__ unsigned long long s_lists[kTop ? kWarps : 1][32];
   __shared__ unsigned long long s_pick[kTop ? kPick : 1], s_last[kTop ? kMaxC * 32 : 1];
-  __shared__ int s_count[2], s_picked[3];  // by the row's number; s_picked is read after the row's last barrier
+  __shared__ int s_count[2], s_picked[3];  // by the row's number; s_picked and s_bound are read after the row's last barrier
   __shared__ uint4 s_ends[2];
-  __shared__ __align__(16) uint32_t s_bound[2][kWarps];  // by the row's parity: the warps' j-th largest values, 0 for none
+  __shared__ __align__(16) uint32_t s_bound[3][kWarps];  // by the row's number: the warps' j-th largest values, 0 for none
   constexpr int kPer = Vec<kBF16>::kPer;
   constexpr int kElt = kBF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   };
 
   if (kTop) {
-    if (tid < 2 * kWarps) s_bound[tid / kWarps][tid % kWarps] = 0u;
+    if (tid < 3 * kWarps) s_bound[tid / kWarps][tid % kWarps] = 0u;
     if (tid == 0) s_count[0] = s_count[1] = s_picked[0] = s_picked[1] = s_picked[2] = 0;
     __syncthreads();
   }
@@ -648,8 +648,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     float tv = -INFINITY;  // at least K values of the slice reach it
     bool plain = true;     // the buffers held every key that reaches it
     if (kTop) {  // the next row's; nobody uses them before this row's barriers
-      if (lane == 0) s_bound[buf ^ 1][warp] = 0u;
-      if (tid == 0) s_count[buf ^ 1] = s_picked[turn3 == 2 ? 0 : turn3 + 1] = 0;
+      const int next3 = turn3 == 2 ? 0 : turn3 + 1;
+      if (lane == 0) s_bound[next3][warp] = 0u;
+      if (tid == 0) s_count[buf ^ 1] = s_picked[next3] = 0;
     }
     if (on) {
       const int t = __ldg(p.tok + ent);
@@ -680,10 +681,10 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
             const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
             if (lane == __ffs(who) - 1) x = 0u;
           }
-          if (lane == 0) *const_cast<volatile uint32_t*>(&s_bound[buf][warp]) = top;
+          if (lane == 0) *const_cast<volatile uint32_t*>(&s_bound[turn3][warp]) = top;
         };
         auto bound = [&]() {
-          const uint32_t t = nth_largest(s_bound[buf], tr, lane);
+          const uint32_t t = nth_largest(s_bound[turn3], tr, lane);
           if (t != 0u) tv = fmaxf(tv, key_value((unsigned long long)t << 32));
         };
         // one round's sums; rm: the largest of its values (NaN if one is)
@@ -922,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         st_cluster_f32(base + 4, b.s);
         st_cluster_f32(base + 8, b.u);
       }
-      if (kTop && lane < kWarps) st_cluster_u32(base + 16 + 4 * lane, plain ? s_bound[buf][lane] : 0u);
+      if (kTop && lane < kWarps) st_cluster_u32(base + 16 + 4 * lane, plain ? s_bound[turn3][lane] : 0u);
       if (kTop && n <= 32) {
         st_cluster_u64(base + 16 + 4 * kWarps + 8 * lane, lane < n ? s_pick[lane] : 0ull);
       } else if (kTop) {
