@@ -17,7 +17,9 @@
 // to 256 rows x 64 dims each, the pair holds the other half; 4 stages of 16 KB,
 // more smaller ones when the tiles are small), fetched by
 // node from the caller's list: a unit is a node's heads or an even share of
-// them (padded to 8 rows, at most 128), which are consecutive rows of q.
+// them (padded to 8 rows, at most 128), which are consecutive rows of q. Units
+// that follow one another come in one box (4 x 8192 rows x 32768 keys: 962 ->
+// 946 us).
 // The issuing thread's own steps bound small tiles: two waits, four MMAs and
 // two commits per 64 dims took it 670 cycles whatever the tile's size. So a
 // stage has one commit, which releases its query rows and, in an item's last
@@ -89,6 +91,7 @@ struct Params {
   int unit;              // query rows of one unit (a multiple of 8, at most 128)
   int chunks;            // units per node
   int per_half;          // units that fit half a tile's 128 columns
+  int adjacent;          // the rows of one unit follow those of the one before (every node, no padding)
   int per_tile;          // stages of a tile
   int row_bytes;         // of one slab of a stage's query rows
   int stages, stage_bytes;  // of the ring of query rows
@@ -162,7 +165,9 @@ struct Tile {
 // kKps: slabs of one stage
 template <int kKps>
 __global__ void __launch_bounds__(kThreads, 1)
-    cache_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, Params p) {
+    cache_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_pair, const __grid_constant__ CUtensorMap tm_half,
+                            Params p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sA = smem_u32(smem), sB = sA + (uint32_t)(p.slabs * kSlabBytes);
@@ -194,6 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_pair);
+    prefetch_tmap(&tm_half);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&s.tmem), 512);
@@ -331,13 +338,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < p.per_tile; ++j) keys(j);
       for (int u = u0; u < u1 && ok; u += per) {
         const Tile tile(p, u, u1, per);
-        const bool mine = lane < (leader ? tile.h0 : tile.nu - tile.h0);
+        // as few boxes as the rows allow: this CTA's whole half, a node's two
+        // units, or single ones
+        const int first = u + (leader ? 0 : tile.h0), count = leader ? tile.h0 : tile.nu - tile.h0;
+        const bool half = p.adjacent && count * p.unit == 128, pairs = p.chunks == 2 && (first & 1) == 0 && (count & 1) == 0;
+        const int step = half ? count : pairs ? 2 : 1;
+        const CUtensorMap* map = half ? &tm_half : pairs ? &tm_pair : &tm_q;
+        const bool mine = lane * step < count;
         int yq = 0;
         if (mine) {
-          const int un = u + (leader ? 0 : tile.h0) + lane, e = un / p.chunks, c = un - e * p.chunks;
+          const int un = first + lane * step, e = un / p.chunks, c = un - e * p.chunks;
           yq = (b * w.N + (list ? __ldg(list + e) : e)) * w.H + c * p.unit;
         }
-        const uint32_t dst = sB + (uint32_t)(lane * p.unit * 128);
+        const uint32_t dst = sB + (uint32_t)(lane * step * p.unit * 128);
         for (int j = 0; j < p.per_tile; ++j) {
           if (u == u0 && !ahead) {
             // the keys of this stage are free when the last tile's stage j is
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kKps; ++i)
               if (i < n)
-                tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes + i * p.row_bytes), &tm_q, 64 * (k0 + i), yq,
+                tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes + i * p.row_bytes), map, 64 * (k0 + i), yq,
                                  bfull0 + 8u * (uint32_t)slot);
           if (++slot == p.stages) {
             slot = 0;
@@ -641,9 +654,12 @@ static int launch(Params p, int max_cache_len, cudaStream_t stream) {
   const WeightsParams& w = p.w;
   const int pairs = device_pairs<kKps>();
   if (pairs <= 0) return DDT_ERR_CUDA;
-  CUtensorMap tk, tq;
+  CUtensorMap tk, tq, tp, th;
+  const uint64_t q_rows = (uint64_t)w.B * w.N * w.H;
   if (!make_map(&tk, w.kv, (uint64_t)w.d_qk, (uint64_t)w.kv_rows, kKeys) ||
-      !make_map(&tq, w.q, (uint64_t)w.d_qk, (uint64_t)w.B * w.N * w.H, (uint32_t)p.unit))
+      !make_map(&tq, w.q, (uint64_t)w.d_qk, q_rows, (uint32_t)p.unit) ||
+      !make_map(&tp, w.q, (uint64_t)w.d_qk, q_rows, (uint32_t)std::min(128, 2 * p.unit)) ||
+      !make_map(&th, w.q, (uint64_t)w.d_qk, q_rows, 128))
     return DDT_ERR_CUDA;
   for (p.b0 = 0; p.b0 < w.B; p.b0 += kMaxB) {
     p.nb = std::min(kMaxB, w.B - p.b0);
@@ -665,7 +681,7 @@ static int launch(Params p, int max_cache_len, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, cache_weights_tc_kernel<kKps>, tk, tq, p) != cudaSuccess) return DDT_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, cache_weights_tc_kernel<kKps>, tk, tq, tp, th, p) != cudaSuccess) return DDT_ERR_CUDA;
   }
   return DDT_OK;
 }
@@ -691,6 +707,7 @@ int launch_cache_weights_tc(WeightsParams w, int max_cache_len, void* workspace,
     }
   }
   p.per_half = 128 / p.unit;
+  p.adjacent = !w.nodes && p.unit * p.chunks == w.H;
   // stages as large as half a tile of this launch can be
   const long long units = std::min(2LL * p.per_half, (long long)w.M * p.chunks);
   p.row_bytes = (int)(((units + 1) / 2 * p.unit + 31) / 32 * 32 * 128);
