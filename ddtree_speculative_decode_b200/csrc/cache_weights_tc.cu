@@ -334,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = k0; k < k1; ++k)
           tma_load_2d_pair(sA + (uint32_t)(k * kSlabBytes), &tm_k, 64 * k, yk, afull0 + 8u * (uint32_t)j);
       };
-      if (ahead && lane == 0)
-        for (int j = 0; j < p.per_tile; ++j) keys(j);
+      if (ahead && lane < p.per_tile) keys(lane);  // a lane per stage: one after the other took 2100 cycles
       for (int u = u0; u < u1 && ok; u += per) {
         const Tile tile(p, u, u1, per);
         // as few boxes as the rows allow: this CTA's whole half, a node's two
@@ -344,13 +343,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool half = p.adjacent && count * p.unit == 128, pairs = p.chunks == 2 && (first & 1) == 0 && (count & 1) == 0;
         const int step = half ? count : pairs ? 2 : 1;
         const CUtensorMap* map = half ? &tm_half : pairs ? &tm_pair : &tm_q;
-        const bool mine = lane * step < count;
+        // lane = box + boxes * slab of the stage
+        const int boxes = (count + step - 1) / step, box = kKps == 1 ? lane : lane % max(boxes, 1);
+        const int slab = kKps == 1 ? 0 : lane / max(boxes, 1);
+        const bool mine = box < boxes && slab < kKps;
         int yq = 0;
         if (mine) {
-          const int un = first + lane * step, e = un / p.chunks, c = un - e * p.chunks;
+          const int un = first + box * step, e = un / p.chunks, c = un - e * p.chunks;
           yq = (b * w.N + (list ? __ldg(list + e) : e)) * w.H + c * p.unit;
         }
-        const uint32_t dst = sB + (uint32_t)(lane * step * p.unit * 128);
+        const uint32_t dst = sB + (uint32_t)(box * step * p.unit * 128 + slab * p.row_bytes);
         for (int j = 0; j < p.per_tile; ++j) {
           if (u == u0 && !ahead) {
             // the keys of this stage are free when the last tile's stage j is
@@ -371,12 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar(kBarBFull + slot), (uint32_t)(n * tile.nu * p.unit * 128));
           __syncwarp();
           ++issued;
-          if (mine)
-#pragma unroll
-            for (int i = 0; i < kKps; ++i)
-              if (i < n)
-                tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes + i * p.row_bytes), map, 64 * (k0 + i), yq,
-                                 bfull0 + 8u * (uint32_t)slot);
+          if (mine && slab < n)
+            tma_load_2d_pair(dst + (uint32_t)(slot * p.stage_bytes), map, 64 * (k0 + slab), yq, bfull0 + 8u * (uint32_t)slot);
           if (++slot == p.stages) {
             slot = 0;
             phase ^= 1u;
@@ -711,7 +709,7 @@ int launch_cache_weights_tc(WeightsParams w, int max_cache_len, void* workspace,
   // stages as large as half a tile of this launch can be
   const long long units = std::min(2LL * p.per_half, (long long)w.M * p.chunks);
   p.row_bytes = (int)(((units + 1) / 2 * p.unit + 31) / 32 * 32 * 128);
-  const int kps = 3 * p.row_bytes <= kRingBytes / 4 ? 3 : 1;
+  const int kps = 3 * p.row_bytes <= kRingBytes / 4 && 3 * ((units + 1) / 2) <= 32 ? 3 : 1;
   p.per_tile = (p.slabs + kps - 1) / kps;
   p.stage_bytes = kps * p.row_bytes;
   p.stages = std::min(kMaxStages, kRingBytes / p.stage_bytes);
