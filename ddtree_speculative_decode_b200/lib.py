@@ -187,6 +187,21 @@ def _device(*tensors, stream=None):
     return torch.cuda.device(dev)
 
 
+_F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+
+
+def _fits(t, dtype, shape, dev: int) -> bool:
+    """_check in one expression (and on device `dev`), for calls that come
+    every few microseconds: when one does not fit, the caller runs the checks
+    that say why."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _ready(dev: int, stream) -> bool:
+    """Nothing to switch: the current device is `dev` and the stream its current one."""
+    return dev >= 0 and stream is None and _raw_stream is not None and _cur_device() == dev
+
+
 def _check_out(out: dict, spec: dict):
     """Caller-supplied output tensors: name -> (dtype, shape)."""
     for name, (dtype, shape) in spec.items():
@@ -490,26 +505,42 @@ def token_logprobs(logits: torch.Tensor, tok: torch.Tensor, nodes: Optional[torc
     [B, M] f32, top_logp [B, M, K] f32, top_tok [B, M, K] i32, status [B, M]."""
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits: expected a tensor")
-    if not logits.is_cuda:
-        raise ValueError("logits: must be a CUDA tensor")
-    dt = _dt(logits)
     if logits.dim() != 3 or tok.dim() != 2:
         raise ValueError("expected logits [B, N, V] and tok [B, M]")
     B, N, V = logits.shape
-    step = _row_stride(logits, "logits")
     M = tok.shape[1]
-    _check(tok, "tok", torch.int32, (B, M))
-    if nodes is not None:
-        _check(nodes, "nodes", torch.int32, (B, M))
-    if out is None:
+    dev = logits.get_device()
+    if out is None and dev >= 0:
         out = alloc_logprobs(B, M, K, logits.device)
-    f32, i32 = torch.float32, torch.int32
-    _check_out(out, {"logp": (f32, (B, M)), "entropy": (f32, (B, M)), "top_logp": (f32, (B, M, K)),
-                     "top_tok": (i32, (B, M, K)), "status": (i32, (B, M))})
-    with _device(logits, tok, nodes, *out.values(), stream=stream):
-        st = load().ddt_token_logprobs(_ptr(logits), dt, V, step, _ptr(nodes), _ptr(tok), B, N, M, K,
-                                       _ptr(out["logp"]), _ptr(out["entropy"]), _ptr(out["top_logp"]),
-                                       _ptr(out["top_tok"]), _ptr(out["status"]), _stream(stream))
+    bm, bmk = (B, M), (B, M, K)
+    try:
+        logp, entropy, top_logp, top_tok, status = out["logp"], out["entropy"], out["top_logp"], out["top_tok"], out["status"]
+        fits = (_fits(tok, _I32, bm, dev) and (nodes is None or _fits(nodes, _I32, bm, dev)) and
+                _fits(logp, _F32, bm, dev) and _fits(entropy, _F32, bm, dev) and _fits(top_logp, _F32, bmk, dev) and
+                _fits(top_tok, _I32, bmk, dev) and _fits(status, _I32, bm, dev))
+    except (AttributeError, KeyError, TypeError):
+        fits = False
+    if not (fits and _ready(dev, stream)):
+        if not logits.is_cuda:
+            raise ValueError("logits: must be a CUDA tensor")
+        _check(tok, "tok", _I32, bm)
+        if nodes is not None:
+            _check(nodes, "nodes", _I32, bm)
+        _check_out(out, {"logp": (_F32, bm), "entropy": (_F32, bm), "top_logp": (_F32, bmk), "top_tok": (_I32, bmk),
+                         "status": (_I32, bm)})
+        logp, entropy, top_logp, top_tok, status = out["logp"], out["entropy"], out["top_logp"], out["top_tok"], out["status"]
+    dt, step = _dt(logits), _row_stride(logits, "logits")
+
+    def call(handle):
+        return load().ddt_token_logprobs(logits.data_ptr(), dt, V, step, _ptr(nodes), tok.data_ptr(), B, N, M, K,
+                                         logp.data_ptr(), entropy.data_ptr(), top_logp.data_ptr(), top_tok.data_ptr(),
+                                         status.data_ptr(), handle)
+
+    if fits and _ready(dev, stream):
+        st = call(_raw_stream(dev))
+    else:
+        with _device(logits, tok, nodes, *out.values(), stream=stream):
+            st = call(_stream(stream))
     _raise("ddt_token_logprobs", st)
     return out
 
@@ -537,41 +568,63 @@ def cache_weights(q: torch.Tensor, lse: torch.Tensor, kv: torch.Tensor, score: t
     count, up to the first negative entry, e.g. accept_compact's acc_nodes with
     causal=True. prev [rows] f32: score = decay * prev + weights (pass score
     itself to accumulate; None: the weights alone). Returns score."""
-    _check(q, "q", (torch.float32, torch.bfloat16))
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or not q.is_contiguous():
+        _check(q, "q", (_F32, _BF16))
     if q.dim() != 4:
         raise ValueError("q: expected [B, N, H, d_qk]")
     B, N, H, d = q.shape
-    _check(lse, "lse", torch.float32, (B, N, H))
-    _check(kv, "kv", q.dtype)
-    if kv.dim() != 2 or kv.shape[1] != d:
+    dev, dt = q.get_device(), _dt(q)
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 2:
         raise ValueError("kv: expected [rows, d_qk]")
     rows = kv.shape[0]
-    _check(score, "score", torch.float32, (rows,))
-    _check(cache_off, "cache_off", torch.int64, (B,))
-    _check(cache_len, "cache_len", torch.int32, (B,))
-    _check(n_nodes, "n_nodes", torch.int32, (B,))
     M = 0
     if nodes is not None:
         if nodes.dim() != 2:
             raise ValueError("nodes: expected [B, M]")
         M = nodes.shape[1]
-        _check(nodes, "nodes", torch.int32, (B, M))
-    if prev is not None:
-        _check(prev, "prev", torch.float32, (rows,))
-    if status is not None:
-        _check(status, "status", torch.int32, (B,))
     if workspace is None:
-        need = cache_weights_workspace_size(B, M if nodes is not None else N, H, d, max_cache_len, q.dtype)
+        need = cache_weights_workspace_size(B, M if nodes is not None else N, H, d, int(max_cache_len), q.dtype)
         if need > 0:
             workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    else:
-        _check(workspace, "workspace", None)
+    b, r = (B,), (rows,)
+    try:
+        fits = (_fits(lse, _F32, (B, N, H), dev) and _fits(kv, q.dtype, (rows, d), dev) and _fits(score, _F32, r, dev) and
+                _fits(cache_off, _I64, b, dev) and _fits(cache_len, _I32, b, dev) and _fits(n_nodes, _I32, b, dev) and
+                (nodes is None or _fits(nodes, _I32, (B, M), dev)) and (prev is None or _fits(prev, _F32, r, dev)) and
+                (status is None or _fits(status, _I32, b, dev)) and
+                (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except AttributeError:
+        fits = False
+    if not (fits and _ready(dev, stream)):
+        _check(lse, "lse", _F32, (B, N, H))
+        _check(kv, "kv", q.dtype)
+        if kv.shape[1] != d:
+            raise ValueError("kv: expected [rows, d_qk]")
+        _check(score, "score", _F32, r)
+        _check(cache_off, "cache_off", _I64, b)
+        _check(cache_len, "cache_len", _I32, b)
+        _check(n_nodes, "n_nodes", _I32, b)
+        if nodes is not None:
+            _check(nodes, "nodes", _I32, (B, M))
+        if prev is not None:
+            _check(prev, "prev", _F32, r)
+        if status is not None:
+            _check(status, "status", _I32, b)
+        if workspace is not None:
+            _check(workspace, "workspace", None)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device(q, lse, kv, score, cache_off, cache_len, n_nodes, nodes, prev, status, workspace, stream=stream):
-        st = load().ddt_cache_weights(_ptr(q), _ptr(lse), _ptr(kv), rows, _ptr(cache_off), _ptr(cache_len),
-                                      _ptr(nodes), _ptr(n_nodes), B, N, M, H, d, float(scale), 1 if causal else 0,
-                                      int(max_cache_len), _dt(q), _ptr(prev), float(decay), _ptr(score),
-                                      _ptr(status), _ptr(workspace), wbytes, _stream(stream))
+
+    def call(handle):
+        return load().ddt_cache_weights(q.data_ptr(), lse.data_ptr(), kv.data_ptr(), rows, cache_off.data_ptr(),
+                                        cache_len.data_ptr(), _ptr(nodes), n_nodes.data_ptr(), B, N, M, H, d, scale,
+                                        1 if causal else 0, int(max_cache_len), dt, _ptr(prev), decay, score.data_ptr(),
+                                        _ptr(status), _ptr(workspace), wbytes, handle)
+
+    if fits and _ready(dev, stream):
+        st = call(_raw_stream(dev))
+    else:
+        with _device(q, lse, kv, score, cache_off, cache_len, n_nodes, nodes, prev, status, workspace, stream=stream):
+            st = call(_stream(stream))
     _raise("ddt_cache_weights", st)
     return score
 
@@ -593,48 +646,70 @@ def cache_evict(kv: torch.Tensor, score: torch.Tensor, cache_off: torch.Tensor, 
     of a request and sizes src; status (optional, [B] i32) receives each
     request's device status. Returns src [n_layers, B, max_keep] i32 and
     new_len [B] i32 (in place: cache_len unless given in out)."""
-    _check(kv, "kv", (torch.float32, torch.bfloat16))
+    if not isinstance(kv, torch.Tensor) or not kv.is_cuda or not kv.is_contiguous():
+        _check(kv, "kv", (_F32, _BF16))
     if kv.dim() != 2:
         raise ValueError("kv: expected [rows, row_elems]")
     rows, row_elems = kv.shape
     B = cache_len.shape[0]
-    _check(score, "score", torch.float32, (rows,))
-    _check(cache_off, "cache_off", torch.int64, (B,))
-    _check(cache_len, "cache_len", torch.int32, (B,))
-    _check(keep, "keep", torch.int32, (B,))
+    dev, dt = kv.get_device(), _dt(kv)
     d_kv = d_score = d_off = None
     d_rows = d_stride = 0
     if dst is not None:
         d_kv, d_score, d_off = dst["kv"], dst["score"], dst["off"]
         d_stride = int(dst.get("layer_stride_rows", 0))
-        _check(d_kv, "dst[kv]", kv.dtype)
-        if d_kv.dim() != 2 or d_kv.shape[1] != row_elems:
+        if not isinstance(d_kv, torch.Tensor) or d_kv.dim() != 2 or d_kv.shape[1] != row_elems:
             raise ValueError("dst[kv]: expected [rows, row_elems]")
         d_rows = d_kv.shape[0]
-        _check(d_score, "dst[score]", torch.float32, (d_rows,))
-        _check(d_off, "dst[off]", torch.int64, (B,))
     if out is None:
         if max_keep is None:
             max_keep = max(1, int(max_cache_len))
-        out = {"src": torch.empty(n_layers, B, max_keep, dtype=torch.int32, device=kv.device)}
+        out = {"src": torch.empty(n_layers, B, max_keep, dtype=_I32, device=kv.device)}
     if "new_len" not in out:
         out["new_len"] = cache_len if dst is None else torch.empty_like(cache_len)
     if "src" not in out or out["src"].dim() != 3:
         raise ValueError("out: missing src [n_layers, B, max_keep]")
+    src, new_len = out["src"], out["new_len"]
     if max_keep is None:
-        max_keep = out["src"].shape[2]
-    _check_out(out, {"src": (torch.int32, (n_layers, B, max_keep)), "new_len": (torch.int32, (B,))})
-    if status is not None:
-        _check(status, "status", torch.int32, (B,))
+        max_keep = src.shape[2]
     if workspace is None:
         workspace = torch.empty(cache_evict_workspace_size(B, n_layers, max_cache_len), dtype=torch.uint8, device=kv.device)
-    _check(workspace, "workspace", None)
-    with _device(kv, score, cache_off, cache_len, keep, d_kv, d_score, d_off, status, workspace, *out.values(),
-                 stream=stream):
-        st = load().ddt_cache_evict(_ptr(kv), rows, _dt(kv), row_elems, _ptr(score), n_layers, layer_stride_rows,
-                                    _ptr(cache_off), _ptr(cache_len), _ptr(keep), sink, recent, B,
-                                    int(max_cache_len), _ptr(d_kv), d_rows, _ptr(d_score), d_stride, _ptr(d_off),
-                                    _ptr(out["new_len"]), _ptr(out["src"]), max_keep, _ptr(status),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    b, r, lbk = (B,), (rows,), (n_layers, B, max_keep)
+    try:
+        fits = (_fits(score, _F32, r, dev) and _fits(cache_off, _I64, b, dev) and _fits(cache_len, _I32, b, dev) and
+                _fits(keep, _I32, b, dev) and _fits(src, _I32, lbk, dev) and _fits(new_len, _I32, b, dev) and
+                (status is None or _fits(status, _I32, b, dev)) and workspace.get_device() == dev and
+                workspace.is_contiguous() and
+                (dst is None or (_fits(d_kv, kv.dtype, (d_rows, row_elems), dev) and _fits(d_score, _F32, (d_rows,), dev) and
+                                 _fits(d_off, _I64, b, dev))))
+    except AttributeError:
+        fits = False
+    if not (fits and _ready(dev, stream)):
+        _check(score, "score", _F32, r)
+        _check(cache_off, "cache_off", _I64, b)
+        _check(cache_len, "cache_len", _I32, b)
+        _check(keep, "keep", _I32, b)
+        if dst is not None:
+            _check(d_kv, "dst[kv]", kv.dtype)
+            _check(d_score, "dst[score]", _F32, (d_rows,))
+            _check(d_off, "dst[off]", _I64, b)
+        _check_out(out, {"src": (_I32, lbk), "new_len": (_I32, b)})
+        if status is not None:
+            _check(status, "status", _I32, b)
+        _check(workspace, "workspace", None)
+
+    def call(handle):
+        return load().ddt_cache_evict(kv.data_ptr(), rows, dt, row_elems, score.data_ptr(), n_layers, layer_stride_rows,
+                                      cache_off.data_ptr(), cache_len.data_ptr(), keep.data_ptr(), sink, recent, B,
+                                      int(max_cache_len), _ptr(d_kv), d_rows, _ptr(d_score), d_stride, _ptr(d_off),
+                                      new_len.data_ptr(), src.data_ptr(), max_keep, _ptr(status), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), handle)
+
+    if fits and _ready(dev, stream):
+        st = call(_raw_stream(dev))
+    else:
+        with _device(kv, score, cache_off, cache_len, keep, d_kv, d_score, d_off, status, workspace, src, new_len,
+                     stream=stream):
+            st = call(_stream(stream))
     _raise("ddt_cache_evict", st)
     return out
