@@ -23,6 +23,11 @@
  *                       Context": greedy tree-accept kernel, KV cache with
  *                       post-verify compaction).
  *
+ * Three more calls serve what a step leaves behind: ddt_token_logprobs (the
+ * committed tokens' log-probs, the rows' entropy and alternatives),
+ * ddt_cache_weights (the attention each cached row received) and
+ * ddt_cache_evict (a cache down to its budget by those weights).
+ *
  * Common conventions
  *   - Every pointer argument is DEVICE memory owned by the caller, except where
  *     a comment says "host". The library allocates no device memory: scratch
