@@ -202,6 +202,8 @@ struct Max<true> {
   __device__ __forceinline__ static __nv_bfloat162 h(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   __device__ __forceinline__ explicit Max(const uint4& r) : v(__hmax2_nan(__hmax2_nan(h(r.x), h(r.y)), __hmax2_nan(h(r.z), h(r.w)))) {}
   __device__ __forceinline__ void add(const Max& o) { v = __hmax2_nan(v, o.v); }
+  // nothing computed from it may move above this point
+  __device__ __forceinline__ void pin() { asm volatile("" : "+r"(*reinterpret_cast<uint32_t*>(&v))); }
   __device__ __forceinline__ float value() const { return max_nan(__low2float(v), __high2float(v)); }
 };
 template <>
@@ -212,6 +214,7 @@ struct Max<false> {
     v = max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)), max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
   __device__ __forceinline__ void add(const Max& o) { v = max_nan(v, o.v); }
+  __device__ __forceinline__ void pin() { asm volatile("" : "+f"(v)); }
   __device__ __forceinline__ float value() const { return v; }
 };
 
@@ -350,17 +353,14 @@ __device__ __noinline__ void careful_keys(const unsigned char* row, int V, int f
 
 // The r-th largest of the warps' published values (0 if fewer are published).
 __device__ __forceinline__ uint32_t nth_largest(const uint32_t* values, int r, int lane) {
-  const volatile uint32_t* v = values;
-  const uint32_t x = v[lane % kWarps];
-  int more = 0, same = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const uint32_t y = __shfl_sync(DDT_FULL_MASK, x, i);
-    more += y > x ? 1 : 0;
-    same += y == x ? 1 : 0;
+  uint32_t x = lane < kWarps ? *const_cast<const volatile uint32_t*>(values + lane) : 0u, top = 0u;
+#pragma unroll 1
+  for (int i = 0; i < r; ++i) {
+    top = __reduce_max_sync(DDT_FULL_MASK, x);
+    const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
+    if (lane == __ffs(who) - 1) x = 0u;
   }
-  const unsigned who = __ballot_sync(DDT_FULL_MASK, more < r && more + same >= r);
-  return __shfl_sync(DDT_FULL_MASK, x, __ffs(who) - 1);
+  return top;
 }
 
 template <bool kBF16, bool kTop>
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         // warp's lanes append together: a place in the warp's buffer is a vote
         // and a count, no atomics. Keys beyond the buffer's end are lost, but
         // counted.
-        auto top = [&](const Max<kBF16> (&vm)[kU], float rm, int r, const unsigned char* from, int at) {
+        auto top = [&](Max<kBF16> (&vm)[kU], float rm, int r, const unsigned char* from, int at) {
           if (r == 0 || r == 2 || r == 8) {
             publish();
             if (r == 0) __syncthreads();  // a first bound needs every warp's
@@ -762,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
           unsigned um = 0u;
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
+            vm[u].pin();
             const float x = vm[u].value();
             um |= x >= tv && x > -INFINITY ? 1u << u : 0u;
           }
