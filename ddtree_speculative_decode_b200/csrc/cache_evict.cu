@@ -40,6 +40,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kRank = 512;           // keys of a bin that are ranked by counting
 constexpr int kSelKeys = 48 * 1024;  // keys held in shared memory; longer caches re-read their scores
+constexpr int kMaxLen = 1 << 30;  // rows of a request: row numbers are added up in 32 bits
 
 // score order: larger score, larger key; NaN lowest
 __device__ __forceinline__ uint32_t score_key(float x) { return x == x ? float_order_key(x) : 0u; }
@@ -58,12 +59,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   const int layer = (int)(blockIdx.x / (unsigned)p.B), b = (int)(blockIdx.x % (unsigned)p.B);
   const int len = p.cache_len[b], keep = p.keep[b];
   const int64_t off = p.cache_off[b], doff = p.kv_dst ? p.dst_off[b] : off;
-  // the request's verdict, the same on every layer
+  // the request's verdict, the same on every layer (the host has checked that
+  // the layers' stride does not overflow)
   const int count = min(len, keep);
   int st = DDT_OK;
   const int64_t last = (int64_t)(p.n_layers - 1);
-  if (off < 0 || len < 0 || off + len + last * p.layer_stride_rows > p.kv_rows || doff < 0 ||
-      (p.kv_dst && doff + max(count, 0) + last * p.dst_layer_stride_rows > p.dst_rows))
+  const int64_t room = p.kv_rows - len - last * p.layer_stride_rows;
+  const int64_t droom = p.kv_dst ? p.dst_rows - max(count, 0) - last * p.dst_layer_stride_rows : room;
+  if (off < 0 || len < 0 || len > kMaxLen || room < 0 || off > room || doff < 0 || droom < 0 || doff > droom)
     st = DDT_ERR_BOUNDS;
   else if (keep < 0 || (len > keep && (int64_t)keep < (int64_t)p.sink + p.recent))
     st = DDT_ERR_INPUT;
@@ -383,7 +386,7 @@ int launch_cache_evict(EvictParams p, int max_cache_len, void* workspace, cudaSt
   p.plan = static_cast<int2*>(workspace);
   // shared memory for the longest cache the caller announces; a longer one
   // (or one beyond what an SM holds) re-reads its scores instead
-  p.held_keys = std::min(kSelKeys, (max_cache_len + 1023) / 1024 * 1024);
+  p.held_keys = std::min(kSelKeys, (std::min(max_cache_len, kMaxLen) + 1023) / 1024 * 1024);
   const int smem = p.held_keys * 4;
   if (smem > 32 * 1024 && !opt_in()) return DDT_ERR_CUDA;
   const int st = launch_pdl(evict_select_kernel, (unsigned)(p.n_layers * p.B), kSelThreads, (size_t)smem, stream, p);

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) cache_weights_simt_kernel(WeightsPar
       if (__ldg(list + j) >= n) s_bad = 1;
   }
   __syncthreads();
-  const bool oob = off < 0 || len < 0 || off + len > p.kv_rows;
+  const bool oob = off < 0 || len < 0 || off > p.kv_rows - len;
   const int st = oob ? DDT_ERR_BOUNDS : s_bad ? DDT_ERR_INPUT : DDT_OK;
   if (tile0 == 0 && tid == 0 && p.dev_status) p.dev_status[b] = st;
   if (st != DDT_OK) return;

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k < 32) break;
       }
     }
-    const bool oob = off < 0 || len < 0 || off + len > w.kv_rows;
+    const bool oob = off < 0 || len < 0 || off > w.kv_rows - len;
     if (lane == 0) {
       s.len[i] = oob || bad ? -1 : len;
       s.m[i] = oob || bad ? 0 : m;

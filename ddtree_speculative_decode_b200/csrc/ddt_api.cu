@@ -162,6 +162,10 @@ int ddt_cache_evict(void* kv, int64_t kv_rows, int kv_dtype, int row_elems, floa
     return DDT_ERR_INVALID_ARG;
   if (n_layers > 1 && (layer_stride_rows < 1 || (kv_dst && dst_layer_stride_rows < 1))) return DDT_ERR_INVALID_ARG;
   if (kv_dst && (kv_dst == kv || dst_rows < 1 || dst_layer_stride_rows < 0)) return DDT_ERR_INVALID_ARG;
+  if (max_keep > (1 << 30)) return DDT_ERR_INVALID_ARG;  // row numbers are added up in 32 bits
+  // the last layer's first row, which the kernels add up in 64 bits
+  if (layer_stride_rows > INT64_MAX / 2 / n_layers || dst_layer_stride_rows > INT64_MAX / 2 / n_layers)
+    return DDT_ERR_INVALID_ARG;
   if (kv_dtype != DDT_F32 && kv_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
   const long long row_bytes = (long long)row_elems * (kv_dtype == DDT_F32 ? 4 : 2);
   if (row_bytes % 4 != 0 || row_bytes > (1 << 20)) return DDT_ERR_INVALID_ARG;

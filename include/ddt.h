@@ -539,7 +539,7 @@ DDT_API int ddt_cache_weights(const void* q, const float* lse, const void* kv, i
  *   int32 (may be cache_len itself); src [n_layers][B][max_keep] int32 (-1
  *   behind the kept rows); dev_status [B] int32 (nullable): DDT_OK;
  *   DDT_ERR_BOUNDS when rows of the request lie outside a pool (on any
- *   layer); DDT_ERR_INPUT when keep[b] < 0, or len > keep[b] < sink +
+ *   layer), or when there are more than 2^30 of them; DDT_ERR_INPUT when keep[b] < 0, or len > keep[b] < sink +
  *   recent; DDT_ERR_CAPACITY when min(len, keep[b]) > max_keep. Each of these
  *   skips the request: nothing moves, src is -1, new_len is cache_len[b] in
  *   place and 0 otherwise.

@@ -190,6 +190,26 @@ def test_statuses_and_skipped_requests():
 
 
 @gpu
+def test_offsets_at_the_64_bit_limit_are_out_of_bounds():
+    kv, score, off, at = make([100, 100, 100], 2, 16, torch.float32, 1)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    offs = torch.tensor([2 ** 63 - 1, off[1], 2 ** 63 - 60], device=DEV)
+    cl, status = torch.tensor([100] * 3, **i32), torch.full((3,), 9, **i32)
+    dkv = kv.to(DEV)
+    lib.cache_evict(dkv, score.to(DEV), offs, cl, torch.tensor([50] * 3, **i32), 4, 6, 100, n_layers=2,
+                    layer_stride_rows=at, status=status)
+    assert status.tolist() == [lib.DDT_ERR_BOUNDS, 0, lib.DDT_ERR_BOUNDS] and cl.tolist() == [100, 50, 100]
+    for la in range(2):
+        assert torch.equal(dkv[la * at + off[0]:la * at + off[0] + 100].cpu(), kv[la * at + off[0]:la * at + off[0] + 100])
+    d2 = {"kv": torch.zeros(400, 16, device=DEV), "score": torch.zeros(400, device=DEV),
+          "off": torch.tensor([0, 2 ** 63 - 10, 100], device=DEV), "layer_stride_rows": 200}
+    cl = torch.tensor([100] * 3, **i32)
+    out = lib.cache_evict(kv.to(DEV), score.to(DEV), torch.tensor(off, device=DEV), cl, torch.tensor([50] * 3, **i32), 4, 6,
+                          100, n_layers=2, layer_stride_rows=at, dst=d2, status=status)
+    assert status.tolist() == [0, lib.DDT_ERR_BOUNDS, 0] and out["new_len"].tolist() == [50, 0, 50]
+
+
+@gpu
 def test_one_pool_holds_source_and_destination():
     """A request moves into a free region of the same pool."""
     kv, score, off, at = make([400], 2, 32, torch.float32, 2)
@@ -302,3 +322,6 @@ def test_host_validation():
     assert call(ws=ctypes.c_void_p(128)) == call(kv=ctypes.c_void_p(258)) == bad
     assert call(kd=q) == call(kd=q, sd=q) == call(od=q) == call(kd=p, sd=q, od=q, rows=5) == call(kd=q, sd=q, od=q) == bad
     assert call(layers=2, kd=q, sd=q, od=q, rows=5) == bad  # no destination layer stride
+    assert call(mk=(1 << 30) + 1) == bad                    # row numbers past 32 bits
+    assert call(layers=3, stride=1 << 62) == bad            # a stride that no pool can have
+    assert call(layers=3, kd=q, sd=q, od=q, rows=5, ds=1 << 62) == bad

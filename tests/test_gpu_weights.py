@@ -265,6 +265,18 @@ def test_statuses(dtype, H, d):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,H,d", [(torch.float32, 4, 80), (torch.bfloat16, 64, 576)])
+def test_offsets_at_the_64_bit_limit_are_out_of_bounds(dtype, H, d):
+    c = make([50, 50], 2, H, d, dtype, 1)
+    c["off"][0] = 2 ** 63 - 1
+    status = torch.full((2,), 9, dtype=torch.int32, device=DEV)
+    got = run(c, status=status)
+    assert status.tolist() == [lib.DDT_ERR_BOUNDS, 0]
+    wrote = got != -7.0
+    assert int(wrote.sum()) == 50 and bool(wrote[c["off"][1]:c["off"][1] + 50].all())
+
+
+@gpu
 def test_repeats_streams_and_graphs():
     """The same bits on every run, with a workspace that is used again and again, on another stream, from two graphs."""
     c = make([2000, 900, 1], 24, 64, 576, torch.bfloat16, 5, nodes=paths(3, 24, 24, 5), causal=True)
