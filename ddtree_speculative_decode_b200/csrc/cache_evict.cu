@@ -4,59 +4,99 @@
 // the first `sink` rows, the last `recent` rows and the best-scored rows
 // between them stay, `keep` in all, in their order.
 //
-// evict_select_kernel: one CTA per (layer, request). Rows become 32-bit keys
-// in score order (protected rows above every score, NaN below every score),
-// held in shared memory. The keep-th largest key T is found by histograms of
-// 2048 bins laid over the keys' own range (so that scores of a few binades
-// still spread over all bins, and few atomics meet), each over the bin of the
-// one before that holds T; a bin of at most 512 keys is finished by counting
-// ranks. Typically one histogram and one count; a bitwise search over the same
-// keys took 32 CTA-wide counts (14 us against 5 for 4096 rows). Rows above T
-// stay, and of those equal to T the lowest ones that fill the number: one
-// ordered pass with a CTA-wide prefix count writes the kept rows' indices and,
-// in place, moves the scores (a score moves to its own index or a lower one,
-// and a chunk is read before it is written).
+// evict_select_kernel: one cluster of C CTAs per (layer, request), C from 1 to 8
+// so that the launch fills the device; each CTA has a slice of the request's
+// rows as 32-bit keys in score order (protected rows above every score, NaN
+// below every score) in shared memory. The keep-th largest key T is found by
+// histograms of 2048 bins laid over the keys' own range (so that scores of a
+// few binades still spread over all bins, and few atomics meet), each over the
+// bin of the one before that holds T; a bin of at most 512 keys is finished by
+// counting ranks. Typically one histogram and one count; a bitwise search over
+// the same keys took 32 CTA-wide counts (14 us against 5 for 4096 rows).
+// Ranges, histograms and counts are joined through distributed shared memory.
+// Rows above T stay, and of those equal to T the lowest ones that fill the
+// number: one ordered pass with prefix counts writes the kept rows' indices.
 //
-// evict_copy_kernel and evict_shift_kernel move the rows. Bound: HBM, each kept
-// row read and written once. Into another region rows go independently: a CTA
-// takes a block of rows (and its scores). In place, row j is written from row src[j] >= j, so row i
-// must be read before it is overwritten: a CTA takes a 128-byte column of a
-// request's rows and walks it upwards in chunks, every chunk read into
-// registers before it is written (later chunks read only rows above the ones
-// written so far, so the next chunk's loads are already under way), and no
-// CTA waits for another. With few layers and requests the columns are as
-// narrow as 32 bytes, for more CTAs. Rows before the first
+// The rows: bound by HBM, each kept row read and written once. Into another
+// region (evict_copy_kernel) rows go independently: a CTA takes a block of rows
+// and their scores. (Letting the selection's clusters copy their own rows, so
+// that one request's selection runs under another's copy, was slower: 82
+// against 60 us for 64 clusters, whose threads keep fewer loads in flight.) In
+// place, row j is written from row src[j] >= j, so row i must be read before it
+// is overwritten: in evict_shift_kernel a CTA takes a 128-byte column of a
+// request's rows (one more CTA their scores) and walks it upwards in chunks,
+// every chunk read into registers before it is written (later chunks read only
+// rows above the ones written so far, so the next chunk's loads are already
+// under way), and no CTA waits for another. With few layers and requests the
+// columns are as narrow as 32 bytes, for more CTAs. Rows before the first
 // evicted one already lie in place and are left alone.
+//
+// Measured (bf16 rows of 576, half of the rows kept unless said; kernels only):
+//   1 x 4096 rows                 11 us, copy; 14 us in place (latency)
+//   1 x 32768 rows                21 us, copy; 50 us in place (few CTAs)
+//   61 layers of 4096 rows        57 us, copy (5.0 TB/s); 65 us in place
+//   16 layers of 4 x 32768 rows   405 us, copy (6.0 TB/s); 484 us in place
 #include <algorithm>
 #include <mutex>
 
 #include "ddt_kernels.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ddt {
 namespace evict {
 
+using sm100::cluster_ctarank;
+using sm100::cluster_sync;
+using sm100::map_to_rank;
+using sm100::smem_u32;
+
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kBinsPer = kBins / kSelThreads;  // of one thread
 constexpr int kRank = 512;           // keys of a bin that are ranked by counting
-constexpr int kSelKeys = 48 * 1024;  // keys held in shared memory; longer caches re-read their scores
+constexpr int kSelKeys = 40 * 1024;  // keys a CTA holds in shared memory; longer slices re-read their scores
+constexpr int kMaxC = 8;
 constexpr int kMaxLen = 1 << 30;  // rows of a request: row numbers are added up in 32 bits
+
+__device__ __forceinline__ uint32_t ld_remote(const void* mine, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(mine), (uint32_t)rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_remote(const void* mine, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(mine), (uint32_t)rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_remote(const void* mine, int rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "r"(map_to_rank(smem_u32(mine), (uint32_t)rank)), "r"(v)
+               : "memory");
+  return old;
+}
 
 // score order: larger score, larger key; NaN lowest
 __device__ __forceinline__ uint32_t score_key(float x) { return x == x ? float_order_key(x) : 0u; }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p) {
   extern __shared__ uint32_t s_key[];
-  __shared__ int s_hist[kBins];
+  __shared__ uint32_t s_hist[kBins], s_sum[kBins];
   __shared__ uint32_t s_rank[kRank];
-  __shared__ uint32_t s_min, s_max, s_T;
-  __shared__ int s_bin, s_above, s_inbin, s_n, s_ties;
+  __shared__ uint32_t s_min, s_max, s_T, s_n;
+  __shared__ uint32_t s_lo[kMaxC], s_hi[kMaxC], s_gt[kMaxC], s_tie[kMaxC], s_first[kMaxC];  // by the cluster's CTA
+  __shared__ int s_bin, s_above, s_inbin, s_ties;
   __shared__ int s_scan[2][kSelWarps];
-  __shared__ int s_hole;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int layer = (int)(blockIdx.x / (unsigned)p.B), b = (int)(blockIdx.x % (unsigned)p.B);
+  const int C = p.cluster, rank = C > 1 ? (int)cluster_ctarank() : 0;
+  auto meet = [&]() {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+  };
+  const unsigned lb = blockIdx.x / (unsigned)C;
+  const int layer = (int)(lb / (unsigned)p.B), b = (int)(lb % (unsigned)p.B);
   const int len = p.cache_len[b], keep = p.keep[b];
   const int64_t off = p.cache_off[b], doff = p.kv_dst ? p.dst_off[b] : off;
   // the request's verdict, the same on every layer (the host has checked that
@@ -72,38 +112,40 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     st = DDT_ERR_INPUT;
   else if (count > p.max_keep)
     st = DDT_ERR_CAPACITY;
-  if (layer == 0 && tid == 0 && p.dev_status) p.dev_status[b] = st;
-  int32_t* src = p.src + ((int64_t)layer * p.B + b) * p.max_keep;
+  const bool head = rank == 0 && tid == 0;
+  if (layer == 0 && head && p.dev_status) p.dev_status[b] = st;
+  int32_t* src = p.src + (int64_t)lb * p.max_keep;
   const int kept = st == DDT_OK ? count : 0;
-  for (int j = kept + tid; j < p.max_keep; j += kSelThreads) src[j] = -1;
-  int2* plan = p.plan + (int64_t)layer * p.B + b;
-  if (st != DDT_OK) {
-    if (tid == 0) *plan = make_int2(-1, 0);
+  for (int j = kept + rank * kSelThreads + tid; j < p.max_keep; j += C * kSelThreads) src[j] = -1;
+  int2* plan = p.plan + lb;
+  if (st != DDT_OK) {  // the same on the whole cluster, as every branch on len and keep
+    if (head) *plan = make_int2(-1, 0);
     return;
   }
-  float* score = p.score + (int64_t)layer * p.layer_stride_rows + off;
+  const float* score = p.score + (int64_t)layer * p.layer_stride_rows + off;
   if (len <= keep) {  // everything stays
-    for (int i = tid; i < len; i += kSelThreads) src[i] = i;
-    if (tid == 0) *plan = make_int2(len, len);
+    for (int i = rank * kSelThreads + tid; i < len; i += C * kSelThreads) src[i] = i;
+    if (head) *plan = make_int2(len, len);
     return;
   }
-  const bool held = len <= p.held_keys;
+  const int per = (len + C - 1) / C, i0 = min(len, rank * per), i1 = min(len, i0 + per);
+  const bool held = per <= p.held_keys;
   const int tail = len - p.recent;
   auto row_key = [&](int i, float x) { return (i < p.sink || i >= tail) ? 0xffffffffu : score_key(x); };
   if (tid == 0) {
-    s_hole = len;
     s_min = 0xffffffffu;
     s_max = 0u;
   }
   __syncthreads();
   // the scored rows between the protected ones; `want` of them stay
   const int m0 = min(p.sink, len), m1 = max(m0, tail), want = keep - (len - (m1 - m0));
+  const int a0 = max(i0, m0), a1 = min(i1, m1);  // of this slice
   {
     uint32_t lo = 0xffffffffu, hi = 0u;
 #pragma unroll 8
-    for (int i = tid; i < len; i += kSelThreads) {
+    for (int i = i0 + tid; i < i1; i += kSelThreads) {
       const uint32_t k = row_key(i, score[i]);
-      if (held) s_key[i] = k;
+      if (held) s_key[i - i0] = k;
       if (i >= m0 && i < m1) {
         lo = min(lo, k);
         hi = max(hi, k);
@@ -116,8 +158,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       atomicMax(&s_max, hi);
     }
   }
+  if (C > 1) {
+    cluster_sync();  // the slice's range is known, and every CTA of the cluster runs
+    if (tid < C) {
+      st_remote(&s_lo[rank], tid, s_min);
+      st_remote(&s_hi[rank], tid, s_max);
+    }
+    cluster_sync();
+    if (tid == 0)
+      for (int c = 0; c < C; ++c) {
+        s_min = min(s_min, s_lo[c]);
+        s_max = max(s_max, s_hi[c]);
+      }
+  }
   __syncthreads();
-  auto key_at = [&](int i) { return held ? s_key[i] : score_key(score[i]); };
+  auto key_at = [&](int i) { return held ? s_key[i - i0] : row_key(i, score[i]); };
 
   // ---- T: kept are the keys above T and, of those equal to it, the first
   // `ties`
@@ -128,18 +183,34 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     int above = 0;  // scored rows above the current range
     for (;;) {      // at most three rounds: 11 bits of the range each
       const int bits = 32 - __clz((int)range), shift = max(0, bits - 11);
-      for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-      if (tid == 0) s_n = 0;
+      for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0u;
+      if (tid == 0) s_n = 0u;
       __syncthreads();
 #pragma unroll 4
-      for (int i = m0 + tid; i < m1; i += kSelThreads) {
+      for (int i = a0 + tid; i < a1; i += kSelThreads) {
         const uint32_t d = key_at(i) - lo;
-        if (d <= range) atomicAdd(&s_hist[d >> shift], 1);
+        if (d <= range) atomicAdd(&s_hist[d >> shift], 1u);
       }
-      __syncthreads();
-      // the bin that holds the want-th largest: thread t has bins 2t, 2t + 1
-      const int h0 = s_hist[2 * tid], h1 = s_hist[2 * tid + 1];
-      int suf = h0 + h1;  // of this thread's and the higher lanes' bins
+      meet();
+      if (C > 1) {
+        // each CTA adds up its share of the bins for everyone
+        const int share = kBins / C, first = rank * share;
+        for (int i = first + tid; i < first + share; i += kSelThreads) {
+          uint32_t n = 0u;
+          for (int c = 0; c < C; ++c) n += ld_remote(&s_hist[i], c);
+          for (int c = 0; c < C; ++c) st_remote(&s_sum[i], c, n);
+        }
+        cluster_sync();
+      }
+      // the bin that holds the want-th largest: thread t has kBinsPer bins
+      const uint32_t* bins = C > 1 ? s_sum : s_hist;
+      int h[kBinsPer], suf = 0;  // of this thread's and the higher lanes' bins
+#pragma unroll
+      for (int q = 0; q < kBinsPer; ++q) {
+        h[q] = (int)bins[kBinsPer * tid + q];
+        suf += h[q];
+      }
+      const int own = suf;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_down_sync(DDT_FULL_MASK, suf, o);
@@ -147,16 +218,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       }
       if (lane == 0) s_scan[0][warp] = suf;
       __syncthreads();
-      const int higher = __reduce_add_sync(DDT_FULL_MASK, lane > warp ? s_scan[0][lane] : 0);
-      const int up1 = above + higher + suf - h0 - h1, up0 = up1 + h1;  // rows above bin 2t + 1, above bin 2t
-      if (up1 < want && want <= up1 + h1) {
-        s_bin = 2 * tid + 1;
-        s_above = up1;
-        s_inbin = h1;
-      } else if (up0 < want && want <= up0 + h0) {
-        s_bin = 2 * tid;
-        s_above = up0;
-        s_inbin = h0;
+      const int higher = __reduce_add_sync(DDT_FULL_MASK, lane > warp && lane < kSelWarps ? s_scan[0][lane] : 0);
+      int up = above + higher + suf - own;  // rows above this thread's bins
+#pragma unroll
+      for (int q = kBinsPer - 1; q >= 0; --q) {
+        if (up < want && want <= up + h[q]) {
+          s_bin = kBinsPer * tid + q;
+          s_above = up;
+          s_inbin = h[q];
+        }
+        up += h[q];
       }
       __syncthreads();
       above = s_above;
@@ -172,11 +243,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
         break;
       }
       range = (1u << shift) - 1u;
-      if (n > kRank) continue;
-      for (int i = m0 + tid; i < m1; i += kSelThreads) {
-        const uint32_t k = key_at(i);
-        if (k - lo <= range) s_rank[atomicAdd(&s_n, 1)] = k;
+      if (n > kRank) {
+        meet();  // nobody reads this round's histogram any more
+        continue;
       }
+      for (int i = a0 + tid; i < a1; i += kSelThreads) {
+        const uint32_t k = key_at(i);
+        if (k - lo <= range) {
+          const uint32_t at = C > 1 ? add_remote(&s_n, 0, 1u) : atomicAdd(&s_n, 1u);
+          st_remote(&s_rank[at], 0, k);
+        }
+      }
+      meet();
+      if (C > 1 && rank > 0)
+        for (int i = tid; i < n; i += kSelThreads) s_rank[i] = ld_remote(&s_rank[i], 0);
       __syncthreads();
       if (tid < n) {
         const uint32_t k = s_rank[tid];
@@ -199,21 +279,47 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     }
   }
 
+  // ---- rows above T and rows equal to it before this slice
+  int base_gt = 0, base_tie = 0;
+  if (C > 1) {
+    int gt = 0, tie = 0;
+    for (int i = i0 + tid; i < i1; i += kSelThreads) {
+      const uint32_t k = key_at(i);
+      gt += k > T ? 1 : 0;
+      tie += k == T ? 1 : 0;
+    }
+    gt = __reduce_add_sync(DDT_FULL_MASK, gt);
+    tie = __reduce_add_sync(DDT_FULL_MASK, tie);
+    if (lane == 0) {
+      s_scan[0][warp] = gt;
+      s_scan[1][warp] = tie;
+    }
+    __syncthreads();
+    gt = __reduce_add_sync(DDT_FULL_MASK, lane < kSelWarps ? s_scan[0][lane] : 0);
+    tie = __reduce_add_sync(DDT_FULL_MASK, lane < kSelWarps ? s_scan[1][lane] : 0);
+    if (tid < C) {
+      st_remote(&s_gt[rank], tid, (uint32_t)gt);
+      st_remote(&s_tie[rank], tid, (uint32_t)tie);
+    }
+    cluster_sync();
+    for (int c = 0; c < rank; ++c) {
+      base_gt += (int)s_gt[c];
+      base_tie += (int)s_tie[c];
+    }
+  }
+
   // ---- the kept rows in order: chunks of four consecutive rows per thread
   __syncthreads();  // s_scan is free
-  int base_gt = 0, base_tie = 0, par = 0, hole = len;
-  for (int c0 = 0; c0 < len; c0 += 4 * kSelThreads) {
-    const int i0 = c0 + 4 * tid;
-    float x[4];
+  int par = 0, hole = len;
+  for (int c0 = i0; c0 < i1; c0 += 4 * kSelThreads) {
+    const int r0 = c0 + 4 * tid;
     uint32_t k[4];
     int mine = 0;  // rows above T in the low half, rows equal to T in the high half
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int i = i0 + q;
-      const bool read = i < len && (!p.kv_dst || !held);  // into another region the copy moves the scores
-      x[q] = read ? score[i] : 0.0f;
-      k[q] = i < len ? (held ? s_key[i] : row_key(i, x[q])) : 0u;
-      if (i < len) mine += k[q] > T ? 1 : k[q] == T ? (1 << 16) : 0;
+      const int i = r0 + q;
+      k[q] = i < i1 ? key_at(i) : 0u;
+      if (i < i1) mine += k[q] > T ? 1 : k[q] == T ? (1 << 16) : 0;
     }
     int inc = mine;
 #pragma unroll
@@ -222,35 +328,40 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       if (lane >= o) inc += y;
     }
     if (lane == 31) s_scan[par][warp] = inc;
-    __syncthreads();  // and every score of the chunk is in registers
-    int before = lane < warp ? s_scan[par][lane] : 0, all = s_scan[par][lane];
-    before = __reduce_add_sync(DDT_FULL_MASK, before);
-    all = __reduce_add_sync(DDT_FULL_MASK, all);
+    __syncthreads();
+    const int w = lane < kSelWarps ? s_scan[par][lane] : 0;
+    int before = __reduce_add_sync(DDT_FULL_MASK, lane < warp ? w : 0);
+    const int all = __reduce_add_sync(DDT_FULL_MASK, w);
     par ^= 1;
     before += inc - mine;
     int gt = base_gt + (before & 0xffff), tie = base_tie + (before >> 16);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int i = i0 + q;
-      if (i >= len) break;
+      const int i = r0 + q;
+      if (i >= i1) break;
       const bool is_gt = k[q] > T, is_tie = k[q] == T;
-      if (is_gt || (is_tie && tie < ties)) {
-        const int j = gt + min(tie, ties);
-        src[j] = i;
-        if (!p.kv_dst && j != i) score[j] = x[q];
-      } else {
-        hole = min(hole, i);
-      }
+      if (is_gt || (is_tie && tie < ties)) src[gt + min(tie, ties)] = i;
+      else hole = min(hole, i);
       gt += is_gt ? 1 : 0;
       tie += is_tie ? 1 : 0;
     }
     base_gt += all & 0xffff;
     base_tie += all >> 16;
   }
+  // the first row that goes: no row before it moves
   hole = __reduce_min_sync(DDT_FULL_MASK, hole);
-  if (lane == 0) atomicMin(&s_hole, hole);
   __syncthreads();
-  if (tid == 0) *plan = make_int2(keep, s_hole);
+  if (tid == 0) s_min = (uint32_t)len;
+  __syncthreads();
+  if (lane == 0) atomicMin(&s_min, (uint32_t)hole);
+  __syncthreads();
+  if (tid == 0) st_remote(&s_first[rank], 0, s_min);
+  meet();  // the slices' lists are complete
+  if (head) {
+    uint32_t first = s_first[0];
+    for (int c = 1; c < C; ++c) first = min(first, s_first[c]);
+    *plan = make_int2(keep, (int)first);
+  }
 }
 
 constexpr int kMoveThreads = 256;
@@ -292,20 +403,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(EvictParams p)
   }
 }
 
-// Rows in place: CTA (layer, request, column of p.col vectors).
+// The shift of one column: rows plan.y .. plan.x - 1, `row` of `step` rows per
+// chunk and step being this thread's.
 template <typename Tv>
-__global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(EvictParams p) {
-  pdl_wait();
-  const unsigned lb = blockIdx.x / (unsigned)p.blocks, blk = blockIdx.x % (unsigned)p.blocks;
-  const int layer = (int)(lb / (unsigned)p.B), b = (int)(lb % (unsigned)p.B);
-  const int2 plan = p.plan[lb];
-  if (layer == 0 && blk == 0 && threadIdx.x == 0) p.new_len[b] = plan.x >= 0 ? plan.x : p.cache_len[b];
-  const int vpr = p.row_vecs;
-  const int c = (int)blk * p.col + (int)threadIdx.x % p.col;
-  const bool on = c < vpr;
-  Tv* kv = reinterpret_cast<Tv*>(p.kv) + ((int64_t)layer * p.layer_stride_rows + p.cache_off[b]) * vpr + c;
-  const int32_t* src = p.src + (int64_t)lb * p.max_keep;
-  const int step = kMoveThreads / p.col, row = (int)threadIdx.x / p.col;
+__device__ __forceinline__ void shift_column(Tv* kv, int stride, bool on, const int32_t* src, int2 plan, int row, int step) {
   // chunk by chunk: the indices two chunks and the rows one chunk ahead
   Tv v[kMoveU];
   int at[kMoveU];
@@ -319,7 +420,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(EvictParams p
   auto rows = [&]() {
 #pragma unroll
     for (int u = 0; u < kMoveU; ++u)
-      if (at[u] >= 0) v[u] = kv[(int64_t)at[u] * vpr];
+      if (at[u] >= 0) v[u] = kv[(int64_t)at[u] * stride];
   };
   indices(plan.y);
   rows();
@@ -334,12 +435,32 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(EvictParams p
 #pragma unroll
     for (int u = 0; u < kMoveU; ++u) {
       const int j = j0 + row + u * step;
-      if (on && j < plan.x) kv[(int64_t)j * vpr] = w[u];
+      if (on && j < plan.x) kv[(int64_t)j * stride] = w[u];
     }
   }
 }
 
-// The selection's shared-memory opt-in, once per device.
+// In place: CTA (layer, request, column of p.col vectors), the last of a
+// request its scores.
+template <typename Tv>
+__global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(EvictParams p) {
+  pdl_wait();
+  const unsigned lb = blockIdx.x / (unsigned)p.blocks, blk = blockIdx.x % (unsigned)p.blocks;
+  const int layer = (int)(lb / (unsigned)p.B), b = (int)(lb % (unsigned)p.B), tid = threadIdx.x;
+  const int2 plan = p.plan[lb];
+  const int64_t row0 = (int64_t)layer * p.layer_stride_rows + p.cache_off[b];
+  if (layer == 0 && blk == 0 && tid == 0) p.new_len[b] = plan.x >= 0 ? plan.x : p.cache_len[b];
+  const int32_t* src = p.src + (int64_t)lb * p.max_keep;
+  if ((int)blk == p.blocks - 1) {
+    shift_column(p.score + row0, 1, true, src, plan, tid, kMoveThreads);
+    return;
+  }
+  const int c = (int)blk * p.col + tid % p.col;
+  shift_column(reinterpret_cast<Tv*>(p.kv) + row0 * p.row_vecs + c, p.row_vecs, c < p.row_vecs, src, plan, tid / p.col,
+               kMoveThreads / p.col);
+}
+
+// Dynamic shared memory of the selection's keys, opted in once per device.
 static bool opt_in() {
   static std::mutex mu;
   static bool done[kMaxDevices] = {false};
@@ -350,6 +471,25 @@ static bool opt_in() {
     done[dev] = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) ==
                 cudaSuccess;
   return done[dev];
+}
+
+static int launch_select(const EvictParams& p, cudaStream_t stream) {
+  if (!opt_in()) return DDT_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.n_layers * p.B * p.cluster));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)p.held_keys * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, p) == cudaSuccess ? DDT_OK : DDT_ERR_CUDA;
 }
 
 template <typename Tv>
@@ -366,7 +506,7 @@ static int launch_move(EvictParams p, cudaStream_t stream) {
   } else {
     p.col = 128 / (int)sizeof(Tv);
     while (p.col * (int)sizeof(Tv) > 32 && lbs * ((p.row_vecs + p.col - 1) / p.col) < 4 * sm_count()) p.col >>= 1;
-    p.blocks = (p.row_vecs + p.col - 1) / p.col;
+    p.blocks = (p.row_vecs + p.col - 1) / p.col + 1;  // and the scores
   }
   if (lbs * p.blocks > 0x7fffffffLL) return DDT_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)(lbs * p.blocks);
@@ -384,12 +524,21 @@ size_t evict_workspace_bytes(int B, int n_layers, int max_cache_len) {
 int launch_cache_evict(EvictParams p, int max_cache_len, void* workspace, cudaStream_t stream) {
   using namespace evict;
   p.plan = static_cast<int2*>(workspace);
-  // shared memory for the longest cache the caller announces; a longer one
-  // (or one beyond what an SM holds) re-reads its scores instead
-  p.held_keys = std::min(kSelKeys, (std::min(max_cache_len, kMaxLen) + 1023) / 1024 * 1024);
-  const int smem = p.held_keys * 4;
-  if (smem > 32 * 1024 && !opt_in()) return DDT_ERR_CUDA;
-  const int st = launch_pdl(evict_select_kernel, (unsigned)(p.n_layers * p.B), kSelThreads, (size_t)smem, stream, p);
+  const long long lbs = (long long)p.n_layers * p.B;
+  // CTAs per (layer, request): as many as there are SMs for, with slices of
+  // 4096 rows and more. A cluster's meetings cost what a few thousand rows do:
+  // with the copy, one request of 4096 rows takes 11 us with one CTA and 13
+  // with four, one of 32768 takes 35 us with one, 23 with four and 21 with
+  // eight; 32 of 32768 take 81 us with one, 68 with four, and 91 with eight,
+  // more CTAs than SMs.
+  p.cluster = kMaxC;
+  while (p.cluster > 1 && (lbs * p.cluster > sm_count() || max_cache_len < 4096 * p.cluster)) p.cluster >>= 1;
+  if (lbs * p.cluster > 0x7fffffffLL) return DDT_ERR_UNSUPPORTED;
+  // shared memory for the longest slice the caller announces; a longer one (or
+  // one beyond what is set aside) re-reads its scores instead
+  const int slice = (std::min(max_cache_len, kMaxLen) + p.cluster - 1) / p.cluster;
+  p.held_keys = std::min(kSelKeys, (slice + 1023) / 1024 * 1024);
+  const int st = launch_select(p, stream);
   if (st != DDT_OK) return st;
   auto al = [](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
   if (p.row_bytes % 16 == 0 && al(p.kv, 16) && al(p.kv_dst, 16)) return launch_move<uint4>(p, stream);

@@ -150,6 +150,7 @@ struct EvictParams {
   int32_t* dev_status;        // [B], nullable
   int2* plan;                 // [n_layers][B]: rows kept (-1: skipped), first row that moves
   int held_keys;              // keys that fit the selection's shared memory
+  int cluster;                // selection CTAs per (layer, request)
   int row_vecs, block_rows, blocks, col;  // the copy's split
 };
 size_t evict_workspace_bytes(int B, int n_layers, int max_cache_len);

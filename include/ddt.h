@@ -548,8 +548,9 @@ DDT_API int ddt_cache_weights(const void* q, const float* lse, const void* kv, i
  *   not overlap in time.
  * Precondition the library cannot check: the layers and requests own
  *   disjoint rows.
- * Two kernels: the selection (one CTA per layer and request) and the copy.
- *   Neither lets a following kernel start early while it writes the pool.
+ * Two kernels: the selection (one to eight CTAs per layer and request) and
+ *   the copy. Neither lets a following kernel start early while it writes the
+ *   pool.
  * Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, alignment, only some of
  *   the destination's pointers, workspace), DDT_ERR_UNSUPPORTED (more than
  *   2^31 - 1 CTAs), DDT_ERR_CUDA (launch).

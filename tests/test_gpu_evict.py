@@ -210,6 +210,17 @@ def test_offsets_at_the_64_bit_limit_are_out_of_bounds():
 
 
 @gpu
+@pytest.mark.parametrize("dst", [False, True])
+@pytest.mark.parametrize("B,layers,n", [(1, 1, 40001), (2, 8, 20001), (5, 7, 12011), (16, 4, 9001), (3, 61, 2050)])
+def test_cluster_splits(B, layers, n, dst):
+    """From one request over eight CTAs to one CTA per layer and request."""
+    lens = [max(1, n - 700 * b) if b % 4 else n for b in range(B)]
+    kv, score, off, at = make(lens, layers, 24, torch.bfloat16, B * layers)
+    score[torch.arange(score.numel()) % 3 == 0] = 0.75  # ties across the slices
+    run(kv, score, lens, off, at, [n // 3 + 1] * B, 3, 100, layers, dst=dst)
+
+
+@gpu
 def test_one_pool_holds_source_and_destination():
     """A request moves into a free region of the same pool."""
     kv, score, off, at = make([400], 2, 32, torch.float32, 2)
