@@ -30,16 +30,16 @@
 // a thread reads only what it copied, so the ring needs no barrier.
 //
 // Top alternatives: packed keys (order-preserving value bits << 32 | ~index:
-// the larger key is the larger value at the lower index). Each warp publishes,
-// after its rounds 0, 2 and 8 and at its end, the j-th largest of its threads'
-// largest values so far; the r-th largest of the warps' is a bound that at
-// least r j >= K values of the slice reach (r = min(K, 4), j = ceil(K / r)),
-// valid however old the published values are, so warps do not wait for one
-// another. A value below the bound costs nothing but its vector's maximum; the
-// others are appended to a buffer in shared memory, cut by the final bound at
-// the end of the slice to few more than K, and sorted by one warp while the
-// others go on. A slice that overruns the buffer (rising rows, rows of few
-// distinct values) is read once more.
+// the larger key is the larger value at the lower index). The pass over the row
+// keeps only, per thread and place in the round (a unit: every 1024th vector),
+// the largest value so far. At the end each warp publishes the j-th largest of
+// its threads' largest values; the r-th largest of the warps' is a bound that
+// at least r j >= K values of the slice reach (r = min(K, 4), j = ceil(K / r)).
+// The few units whose largest value reaches it are read once more, by the whole
+// warp, for the keys of the values that do. (Collecting keys on the way, by a
+// bound that rises with the row, took 5 instructions per logit instead of 1 and
+// had to give up on rising rows.) If more than kPick values reach the bound
+// (rows of few distinct values), the slice is read once more with care.
 #include <algorithm>
 #include <mutex>
 
@@ -65,9 +65,8 @@ constexpr int kMaxC = 8;          // CTAs that may share a row
 constexpr int kOwn = 256;         // rows of one CTA in a launch that follows a node list
 constexpr int kStep = 64;         // threads that add keys between two looks in the careful pass
 constexpr int kBest = 4;          // warps whose published values make the bound
-constexpr int kWarpCand = 96;     // keys of a warp's buffer
-constexpr int kCand = kWarps * kWarpCand;
-constexpr int kPick = 128;        // of these, the ones that reach the final bound
+constexpr int kCand = 768;        // keys of the careful pass's buffer
+constexpr int kPick = 128;        // keys that reach the bound
 constexpr float kFar = -150.0f;   // e^kFar and 2^kFar are zero in float32
 constexpr float kUsual = 1e6f;    // below this, a logit in base 2 is off by less than one before it is rounded
 constexpr float kLn2 = 0.6931471805599453f;
@@ -202,8 +201,6 @@ struct Max<true> {
   __device__ __forceinline__ static __nv_bfloat162 h(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   __device__ __forceinline__ explicit Max(const uint4& r) : v(__hmax2_nan(__hmax2_nan(h(r.x), h(r.y)), __hmax2_nan(h(r.z), h(r.w)))) {}
   __device__ __forceinline__ void add(const Max& o) { v = __hmax2_nan(v, o.v); }
-  // nothing computed from it may move above this point
-  __device__ __forceinline__ void pin() { asm volatile("" : "+r"(*reinterpret_cast<uint32_t*>(&v))); }
   __device__ __forceinline__ float value() const { return max_nan(__low2float(v), __high2float(v)); }
 };
 template <>
@@ -214,7 +211,6 @@ struct Max<false> {
     v = max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)), max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
   __device__ __forceinline__ void add(const Max& o) { v = max_nan(v, o.v); }
-  __device__ __forceinline__ void pin() { asm volatile("" : "+f"(v)); }
   __device__ __forceinline__ float value() const { return v; }
 };
 
@@ -239,14 +235,22 @@ __device__ __noinline__ uint4 load_edge(const unsigned char* row, int V, int ful
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Careful pass: appends the keys of a vector's values that reach T (T's value:
-// tv) to the CTA's buffer.
+// The values of a vector that reach tv, one bit each (no -inf).
 template <bool kBF16>
-__device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, float tv, unsigned long long* cand,
-                                         int* count) {
+__device__ __forceinline__ unsigned hits_of(const uint4& v, float tv) {
   unsigned hits = 0u;
 #pragma unroll
-  for (int q = 0; q < Vec<kBF16>::kPer; ++q) hits |= value_of<kBF16>(v, q) >= tv ? 1u << q : 0u;
+  for (int q = 0; q < Vec<kBF16>::kPer; ++q) {
+    const float x = value_of<kBF16>(v, q);
+    hits |= x >= tv && x > -INFINITY ? 1u << q : 0u;
+  }
+  return hits;
+}
+// Writes their keys to buf[at ..], as far as they fit in room and reach T;
+// place_of gives each its place.
+template <bool kBF16, typename F>
+__device__ __forceinline__ void write_keys(const uint4& v, unsigned hits, int at, unsigned long long T,
+                                           unsigned long long* buf, int room, F place_of) {
   while (hits) {
     const int q = __ffs(hits) - 1;
     hits &= hits - 1u;
@@ -258,11 +262,21 @@ __device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, 
       x = __uint_as_float(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
     }
     const unsigned long long key = topk_key(x, at + q);
-    if (x > -INFINITY && key >= T) {
-      const int slot = atomicAdd(count, 1);
-      if (slot < kCand) cand[slot] = key;
-    }
+    if (key < T) continue;
+    const int slot = place_of();
+    if (slot < room) buf[slot] = key;
   }
+}
+// Careful pass: any number of values, places by count.
+template <bool kBF16>
+__device__ __noinline__ void append_keys(uint4 v, int at, unsigned long long T, float tv, unsigned long long* cand,
+                                         int* count) {
+  write_keys<kBF16>(v, hits_of<kBF16>(v, tv), at, T, cand, kCand, [&]() { return atomicAdd(count, 1); });
+}
+// The keys of one lane's values, from its place on.
+template <bool kBF16>
+__device__ __noinline__ void place_keys(uint4 v, unsigned hits, int at, unsigned long long* buf, int place) {
+  write_keys<kBF16>(v, hits, at, 1ull, buf, kPick, [&]() { return place++; });
 }
 
 // One key per lane into descending order; rolled and out of line, as is the
@@ -311,7 +325,7 @@ __device__ __forceinline__ unsigned long long best_of(const unsigned long long* 
   return l;
 }
 
-// The K best keys of a slice whose values defeat the running bound: its whole
+// The K best keys of a slice of which too many values reach the bound: its whole
 // vectors [v0, v1) once more (and the row's ends, if it has them), kStep
 // threads at a time between looks at the buffer's level, the bound raised to
 // the K-th best key whenever the buffer could run full. Leaves the 32 best.
@@ -374,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   __shared__ unsigned long long s_cand[kTop ? kCand : 1];
   __shared__ unsigned long long s_lists[kTop ? kWarps : 1][32];
   __shared__ unsigned long long s_pick[kTop ? kPick : 1], s_last[kTop ? kMaxC * 32 : 1];
-  __shared__ int s_count[2], s_picked[3];  // by the row's number; s_picked and s_bound are read after the row's last barrier
+  __shared__ int s_count, s_picked[3];  // s_picked, s_bound: by the row's number, read after the row's last barrier
+  __shared__ uint16_t s_unit[kTop ? kWarps : 1][kU * 32];  // a warp's units that reach the bound
   __shared__ uint4 s_ends[2];
   __shared__ __align__(16) uint32_t s_bound[3][kWarps];  // by the row's number: the warps' j-th largest values, 0 for none
   constexpr int kPer = Vec<kBF16>::kPer;
@@ -631,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
 
   if (kTop) {
     if (tid < 3 * kWarps) s_bound[tid / kWarps][tid % kWarps] = 0u;
-    if (tid == 0) s_count[0] = s_count[1] = s_picked[0] = s_picked[1] = s_picked[2] = 0;
+    if (tid == 0) s_picked[0] = s_picked[1] = s_picked[2] = 0;
     __syncthreads();
   }
   int turn3 = 2;  // it mod 3
@@ -646,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
     const bool on = ent >= 0;  // the same for the CTAs of a group
     Sums a = {-INFINITY, 0.0f, 0.0f};
     float tv = -INFINITY;  // at least K values of the slice reach it
-    bool plain = true;     // the buffers held every key that reaches it
+    bool plain = true;     // the buffer held every key that reaches it
     if (kTop) {  // the next row's; nobody uses them before this row's barriers
       const int next3 = turn3 == 2 ? 0 : turn3 + 1;
       if (lane == 0) s_bound[next3][warp] = 0u;
-      if (tid == 0) s_count[buf ^ 1] = s_picked[next3] = 0;
+      if (tid == 0) s_picked[next3] = 0;
     }
     if (on) {
       const int t = __ldg(p.tok + ent);
@@ -743,106 +758,55 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
             }
           }
         };
-        int mine = 0;  // keys this warp appended to its buffer
-        // One round's alternatives: the vectors whose largest value (vm) reaches
-        // the bound are looked at once more where they lie in shared memory,
-        // `from` the first of this thread's; `at` is its first element. The
-        // warp's lanes append together: a place in the warp's buffer is a vote
-        // and a count, no atomics. Keys beyond the buffer's end are lost, but
-        // counted.
-        auto top = [&](Max<kBF16> (&vm)[kU], float rm, int r, const unsigned char* from, int at) {
-          if (r == 0 || r == 2 || r == 8) {
-            publish();
-            if (r == 0) __syncthreads();  // a first bound needs every warp's
-            bound();
-          } else if (r == 1 || (r & 3) == 0) {
-            bound();
-          }
-          if (!__any_sync(DDT_FULL_MASK, rm >= tv && rm > -INFINITY)) return;
-          unsigned um = 0u;
+        Max<kBF16> um[kU];  // the largest values of this thread's units
+        if (kTop) {
 #pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            vm[u].pin();
-            const float x = vm[u].value();
-            um |= x >= tv && x > -INFINITY ? 1u << u : 0u;
-          }
-          while (__any_sync(DDT_FULL_MASK, um != 0u)) {
-            const int u = um ? __ffs(um) - 1 : 0;
-            const unsigned char* vec = from + u * kThreads * 16;
-            const uint4 x = *reinterpret_cast<const uint4*>(vec);
-            unsigned hits = 0u;
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) hits |= value_of<kBF16>(x, q) >= tv ? 1u << q : 0u;
-            if (um == 0u) hits = 0u;
-            um &= um - 1u;
-            unsigned votes;
-            while ((votes = __ballot_sync(DDT_FULL_MASK, hits != 0u)) != 0u) {
-              const int q = hits ? __ffs(hits) - 1 : 0;
-              const float y = kBF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(vec)[q])
-                                    : reinterpret_cast<const float*>(vec)[q];
-              const int place = mine + __popc(votes & ((1u << lane) - 1u));
-              if (hits && place < kWarpCand)
-                s_cand[warp * kWarpCand + place] = y > -INFINITY ? topk_key(y, at + u * kThreads * kPer + q) : 0ull;
-              mine += __popc(votes);
-              hits &= hits - 1u;
-            }
-          }
-        };
-        auto largest = [&](const uint4 (&v)[kU], Max<kBF16> (&vm)[kU]) {
+          for (int u = 0; u < kU; ++u) um[u] = Max<kBF16>(none);
+        }
+        auto largest = [&](const uint4 (&v)[kU]) {
           Max<kBF16> m(v[0]);
-          vm[0] = m;
+          if (kTop) um[0].add(m);
 #pragma unroll
           for (int u = 1; u < kU; ++u) {
-            vm[u] = Max<kBF16>(v[u]);
-            m.add(vm[u]);
+            const Max<kBF16> x(v[u]);
+            if (kTop) um[u].add(x);
+            m.add(x);
           }
           return m.value();
         };
         auto next_slot = [&](uint32_t x) { return x >= (kStages - 1) * kRound * 16 ? x - (kStages - 1) * kRound * 16 : x + kRound * 16; };
-        int left = v1 - v0, r = 0, at = full0 + (v0 + tid) * kPer;
+        int left = v1 - v0;
         // whole rounds: no conditions but the rare ones
 #pragma unroll 1
-        for (; left >= kRound; left -= kRound, ++r, at += kRound * kPer) {
+        for (; left >= kRound; left -= kRound) {
           uint4 v[kU];
           copy_wait<kStages - 1>();
           const unsigned char* from = s_ring + slot;
 #pragma unroll
           for (int u = 0; u < kU; ++u) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
           slot = next_slot(slot);
-          Max<kBF16> vm[kU];
-          const float rm = largest(v, vm);
-          sums(v, rm);
-          if (kTop) top(vm, rm, r, from, at);
+          sums(v, largest(v));
           // this round's slots are free
           if (f_left >= kRound) fetch_round();
           else fetch();
         }
 #pragma unroll 1
-        for (; left > 0 || ends; left -= kRound, ++r, at += kRound * kPer) {
+        for (; left > 0 || ends; left -= kRound) {
           uint4 v[kU];
 #pragma unroll
           for (int u = 0; u < kU; ++u) v[u] = none;
-          int pos = at;
-          const unsigned char* from = s_ring + slot;
           if (left > 0) {
             copy_wait<kStages - 1>();
+            const unsigned char* from = s_ring + slot;
 #pragma unroll
             for (int u = 0; u < kU; ++u)
               if (left > tid + u * kThreads) v[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
             slot = next_slot(slot);
           } else {  // the row's ends
             ends = false;
-            if (tid < 2) {
-              v[0] = load_edge<kBF16>(row, V, full0, full1, tid);
-              s_ends[tid] = v[0];
-              from = reinterpret_cast<const unsigned char*>(&s_ends[tid]);
-              pos = tid == 0 ? full0 - kPer : full1;
-            }
+            if (tid < 2) v[0] = s_ends[tid] = load_edge<kBF16>(row, V, full0, full1, tid);
           }
-          Max<kBF16> vm[kU];
-          const float rm = largest(v, vm);
-          sums(v, rm);
-          if (kTop) top(vm, rm, r, from, pos);
+          sums(v, largest(v));
           if (left > 0) fetch();
         }
         // the given token's logit: its index has arrived by now, and the join
@@ -854,28 +818,74 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
                                        : __ldg(reinterpret_cast<const float*>(row) + t);
         }
         if (kTop) {
-          // of the warps' buffers, the keys that reach the final bound: few
-          // more than K
-          if (r > 0) publish();
-          if (lane == 0 && mine > kWarpCand) s_count[buf] = kCand + 1;
+          publish();
           __syncthreads();
           bound();
-          int n = min(mine, kWarpCand), from = warp * kWarpCand;
-          if (s_count[buf] > kCand) {  // keys were lost: the same for the whole CTA
-            careful_keys<kBF16>(row, V, full0, full1, v0, v1, has_ends, K, s_cand, &s_count[buf], s_lists);
-            n = warp == 0 ? 32 : 0;
-            from = 0;
-            tv = -INFINITY;
-            plain = false;
+          // one vector per lane and place: their keys that reach the bound go to the
+          // CTA's list, in the places of one count
+          auto pick = [&](const uint4 (&x)[kU], const int (&at)[kU]) {
+            unsigned hits[kU];
+            int own = 0;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              hits[u] = Max<kBF16>(x[u]).value() >= tv ? hits_of<kBF16>(x[u], tv) : 0u;
+              own += __popc(hits[u]);
+            }
+            int place = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(DDT_FULL_MASK, place, o);
+              if (lane >= o) place += y;
+            }
+            const int all = __shfl_sync(DDT_FULL_MASK, place, 31);
+            if (all == 0) return true;
+            int base = 0;
+            if (lane == 0) base = atomicAdd(&s_picked[turn3], all);
+            base = __shfl_sync(DDT_FULL_MASK, base, 0);
+            place += base - own;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              if (hits[u]) place_keys<kBF16>(x[u], hits[u], at[u], s_pick, place);
+              place += __popc(hits[u]);
+            }
+            return base + all <= kPick;  // otherwise the careful pass follows
+          };
+          int n = 0;  // units of this warp that reach the bound
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const float m = um[u].value();
+            const bool reach = m >= tv && m > -INFINITY;
+            const unsigned votes = __ballot_sync(DDT_FULL_MASK, reach);
+            if (reach) s_unit[warp][n + __popc(votes & ((1u << lane) - 1u))] = (uint16_t)(u * kThreads + tid);
+            n += __popc(votes);
           }
-          for (int i = 0; i < n; i += 32) {
-            const unsigned long long key = i + lane < n ? s_cand[from + i + lane] : 0ull;
-            const bool keep = key != 0ull && key_value(key) >= tv;
-            const unsigned votes = __ballot_sync(DDT_FULL_MASK, keep);
-            int at = 0;
-            if (lane == 0 && votes) at = atomicAdd(&s_picked[turn3], __popc(votes));
-            at = __shfl_sync(DDT_FULL_MASK, at, 0) + __popc(votes & ((1u << lane) - 1u));
-            if (keep && at < kPick) s_pick[at] = key;
+          __syncwarp();
+          const unsigned char* vecs = row + (long long)full0 * kElt + (long long)v0 * 16;
+          // all vectors of all these units, over the warp's lanes
+          const unsigned per = (unsigned)(v1 - v0 + kRound - 1) / kRound, items = (unsigned)n * per;
+#pragma unroll 1
+          for (unsigned i0 = (unsigned)lane; i0 - (unsigned)lane < items; i0 += 32 * kU) {
+            uint4 x[kU];
+            int at[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              const unsigned i = i0 + 32 * u, unit = i / per;
+              const int k = i < items ? (int)((i - unit * per) * kRound + s_unit[warp][unit]) : v1 - v0;
+              at[u] = full0 + (v0 + k) * kPer;
+              x[u] = k < v1 - v0 ? __ldg(reinterpret_cast<const uint4*>(vecs + (long long)k * 16)) : none;
+            }
+            if (!pick(x, at)) break;
+          }
+          if (has_ends && warp == 0) {
+            uint4 x[kU];
+            int at[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) x[u] = none, at[u] = 0;
+            if (lane < 2) {
+              x[0] = s_ends[lane];
+              at[0] = lane == 0 ? full0 - kPer : full1;
+            }
+            pick(x, at);
           }
         }
         float s0, s1, u0, u1;
@@ -902,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
       share(it, nfull, v0, v1);
       const int full1 = full0 + nfull * kPer;
       careful_keys<kBF16>(row2, V, full0, full1, v0, v1, (full0 > 0 || full1 < V) && (whole || part == 0), K, s_cand,
-                          &s_count[buf], s_lists);
+                          &s_count, s_lists);
       if (warp == 0) s_pick[lane] = s_cand[lane];
       if (tid == 0) s_picked[turn3] = 32;
       plain = false;
