@@ -144,6 +144,26 @@ def test_masked_logits(K, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,V,K", [(1, 50021, 32), (30, 50021, 9), (60, 33000, 20), (1, 163840, 8), (2, 9001, 2)])
+def test_where_the_largest_values_lie(B, V, K, dtype):
+    """The alternatives side by side, a round of vectors apart, at the row's ends, or all but one of them apart from it."""
+    logits, tok = make(B, 9, V, dtype, V + B)
+    high = torch.linspace(16, 31.5, K, device=DEV)
+    logits[:, 0, 1000:1000 + K] = high
+    step = V // K // 1024 * 1024 or V // K
+    logits[:, 1, 17:17 + step * (K - 1) + 1:step] = high
+    logits[:, 2, :K] = high
+    logits[:, 3, V - K:] = high.flip(0)
+    logits[:, 4, 5000:5300] = 20.0                   # more equal values than are listed
+    logits[:, 5, :8] = 20.0                          # and fewer
+    logits[:, 6, 2048:2048 + 8 * K:8] = high         # one per vector of a warp
+    logits[:, 7, V // 2] = 30.0
+    logits[:, 8, ::V // 150] = 20.0                  # equal ones, spread
+    check(logits, tok, K=K)
+
+
+@gpu
 @pytest.mark.parametrize("K", [1, 5, 32])
 @pytest.mark.parametrize("V", [40000, 163840])
 def test_ties_and_order(V, K):
