@@ -525,14 +525,15 @@ int launch_cache_evict(EvictParams p, int max_cache_len, void* workspace, cudaSt
   using namespace evict;
   p.plan = static_cast<int2*>(workspace);
   const long long lbs = (long long)p.n_layers * p.B;
-  // CTAs per (layer, request): as many as there are SMs for, with slices of
-  // 4096 rows and more. A cluster's meetings cost what a few thousand rows do:
-  // with the copy, one request of 4096 rows takes 11 us with one CTA and 13
-  // with four, one of 32768 takes 35 us with one, 23 with four and 21 with
-  // eight; 32 of 32768 take 81 us with one, 68 with four, and 91 with eight,
-  // more CTAs than SMs.
-  p.cluster = kMaxC;
-  while (p.cluster > 1 && (lbs * p.cluster > sm_count() || max_cache_len < 4096 * p.cluster)) p.cluster >>= 1;
+  // CTAs per (layer, request): one for short caches, otherwise as many as there
+  // are SMs for. A cluster's meetings cost what about 8000 rows do: with the
+  // copy, one request of 6000 rows takes 12.6 us with one CTA and 14.2 with
+  // eight, of 12000 16.7 and 15.4, of 32768 28.6 and 17.1 (4096 rows kept); 64
+  // of 8192 take 63 us with one, 65 with two and 75 with four, two per SM.
+  // Clusters of eight do not fill the device (their SMs are neighbours): 16 of
+  // 24000 take 49 us with eight CTAs, 40 with four, 42 with two.
+  p.cluster = max_cache_len < 10240 ? 1 : kMaxC;
+  while (p.cluster > 1 && lbs * p.cluster > (p.cluster > 4 ? sm_count() / 2 : sm_count())) p.cluster >>= 1;
   if (lbs * p.cluster > 0x7fffffffLL) return DDT_ERR_UNSUPPORTED;
   // shared memory for the longest slice the caller announces; a longer one (or
   // one beyond what is set aside) re-reads its scores instead

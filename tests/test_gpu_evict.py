@@ -211,7 +211,7 @@ def test_offsets_at_the_64_bit_limit_are_out_of_bounds():
 
 @gpu
 @pytest.mark.parametrize("dst", [False, True])
-@pytest.mark.parametrize("B,layers,n", [(1, 1, 40001), (2, 8, 20001), (5, 7, 12011), (16, 4, 9001), (3, 61, 2050)])
+@pytest.mark.parametrize("B,layers,n", [(1, 1, 40001), (2, 8, 20001), (5, 7, 12011), (7, 8, 11003), (16, 4, 9001), (3, 61, 2050)])
 def test_cluster_splits(B, layers, n, dst):
     """From one request over eight CTAs to one CTA per layer and request."""
     lens = [max(1, n - 700 * b) if b % 4 else n for b in range(B)]
