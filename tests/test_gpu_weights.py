@@ -147,6 +147,16 @@ def test_row_sizes(d):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 33), (torch.float32, 40), (torch.float32, 576), (torch.bfloat16, 20),
+                                     (torch.bfloat16, 104), (torch.bfloat16, 640)])
+@pytest.mark.parametrize("N,H", [(2, 16), (3, 11), (9, 16), (19, 15)])
+def test_cuda_core_tiles(N, H, d, dtype):
+    """One to three tiles of rows, of both sizes, over keys that end before, at and behind a tile's end."""
+    check(make([127, 128, 129, 1, 300], N, H, d, dtype, N + d))
+    check(make([127, 64, 65, 2, 300], N, H, d, dtype, N + d, nodes=paths(5, N, N, d), causal=True), max_len=100)
+
+
+@gpu
 @pytest.mark.parametrize("dtype,H,d", [(torch.float32, 4, 80), (torch.bfloat16, 64, 576), (torch.bfloat16, 16, 576)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_node_lists(dtype, H, d, causal):
