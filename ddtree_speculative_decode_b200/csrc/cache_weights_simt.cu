@@ -9,7 +9,7 @@
 // time: a 128 x 128 tile of dot products in registers (8 keys x 8 rows per
 // thread, 64 products for 16 values read from shared memory, two CTAs per SM),
 // operands through two stages of 16 dims, the next one's loads in flight under
-// this one's products. Up to 32 rows the tile is 64 x 32 with stages of 32 dims
+// this one's products. For few rows the tile is 64 x 32 with stages of 32 dims
 // (fewer trips: their loads' latency is all that counts). Each key belongs to
 // one CTA, so its sum is formed in a fixed order (per thread over the row
 // tiles, then over the 16 threads that share the key) without atomics. Bound by
@@ -215,11 +215,18 @@ static int launch_tile(WeightsParams p, int max_cache_len, cudaStream_t stream) 
 }
 template <typename T>
 static int launch_type(const WeightsParams& p, int max_cache_len, cudaStream_t stream) {
-  // The large tile if there are rows for more than a small one, however few
-  // keys: 256 rows of 128 x 8192 keys take 39 us with 64 large tiles and 47 with
-  // 128 small ones, 48 rows x 4 x 8192 keys 33 and 40 us.
-  const long long rows = (long long)(p.nodes ? p.M : p.N) * p.H;
-  return rows > 32 ? launch_tile<T, 8, 8>(p, max_cache_len, stream) : launch_tile<T, 4, 2>(p, max_cache_len, stream);
+  // The shorter estimated time: waves of two CTAs per SM times tiles of rows,
+  // of which a large one takes 3.2 times a small one's time (128 dims: 17 and
+  // 5.4 us, the latter mostly latency). 256 rows x 8192 keys: 39 us with 64
+  // large tiles, 47 with 128 small ones; 4 x 48 rows x 8192 keys: 33 and 40; 35
+  // rows x 536 keys of 40 dims: 11.1 and 7.3.
+  const long long rows = (long long)(p.nodes ? p.M : p.N) * p.H, slots = 2LL * sm_count();
+  auto time = [&](long long keys, long long rows_per, int unit) {
+    const long long ctas = (max_cache_len / keys + 1) * p.B;
+    return (ctas + slots - 1) / slots * ((rows + rows_per - 1) / rows_per) * unit;
+  };
+  return time(128, 128, 32) <= time(64, 32, 10) ? launch_tile<T, 8, 8>(p, max_cache_len, stream)
+                                                : launch_tile<T, 4, 2>(p, max_cache_len, stream);
 }
 
 }  // namespace cw

@@ -40,6 +40,11 @@
 // bound that rises with the row, took 5 instructions per logit instead of 1 and
 // had to give up on rising rows.) If more than kPick values reach the bound
 // (rows of few distinct values), the slice is read once more with care.
+//
+// Measured (bf16, rows of 163840; us): 512 rows 34.7 without alternatives, 45
+// with 8, 58 with 32; 2048 rows 111 without (6.0 TB/s), 136 with 8; 4096 rows
+// 244 with one (5.5 TB/s); instructions per logit 7.7 with none or one, 9.7
+// with 8, of which the row's end is the difference.
 #include <algorithm>
 #include <mutex>
 
@@ -154,7 +159,11 @@ __device__ __forceinline__ Sums join(Sums a) {
 __device__ __forceinline__ int rank_of(unsigned long long key, const unsigned long long* keys, int n) {
   int r = 0;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) r += keys[i] > key ? 1 : 0;
+  for (int i = 0; i + 1 < n; i += 2) {
+    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(keys + i);
+    r += (k.x > key ? 1 : 0) + (k.y > key ? 1 : 0);
+  }
+  if (n & 1) r += keys[n - 1] > key ? 1 : 0;
   return r;
 }
 
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   __shared__ __align__(16) Part s_part[2][kMaxC];
   __shared__ unsigned long long s_cand[kTop ? kCand : 1];
   __shared__ unsigned long long s_lists[kTop ? kWarps : 1][32];
-  __shared__ unsigned long long s_pick[kTop ? kPick : 1], s_last[kTop ? kMaxC * 32 : 1];
+  __shared__ __align__(16) unsigned long long s_pick[kTop ? kPick : 1], s_last[kTop ? kMaxC * 32 : 1];
   __shared__ int s_count, s_picked[3];  // s_picked, s_bound: by the row's number, read after the row's last barrier
   __shared__ uint32_t s_max[kTop ? kThreads : 1];  // the threads' largest values, upper halves of their keys
   __shared__ uint16_t s_unit[kTop ? kWarps : 1][kU * 32];  // a warp's units that reach the bound
@@ -692,9 +701,10 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
         // this warp's tj-th largest of its threads' largest values
         auto publish = [&]() {
           uint32_t x = a.m > -INFINITY ? float_order_key(a.m) : 0u, top = 0u;
+          const bool enough = __popc(__ballot_sync(DDT_FULL_MASK, x != 0u)) >= tj;  // otherwise it publishes none
           if (K > kFew) s_max[tid] = x >> 16;
 #pragma unroll 1
-          for (int q = 0; q < tj; ++q) {
+          for (int q = 0; enough && q < tj; ++q) {
             top = __reduce_max_sync(DDT_FULL_MASK, x);
             const unsigned who = __ballot_sync(DDT_FULL_MASK, x == top);
             if (lane == __ffs(who) - 1) x = 0u;
