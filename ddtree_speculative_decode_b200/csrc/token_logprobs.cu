@@ -360,8 +360,10 @@ __device__ __noinline__ void careful_keys(const unsigned char* row, int V, int f
       append_keys<kBF16>(x, pos, T, T == 1ull ? -INFINITY : key_value(T), cand, count);
     }
     __syncthreads();
-    if (*count > kCand - kStep * 8) {  // the same for the whole CTA
-      const unsigned long long l = best_of(cand, *count, lists, warp, lane);
+    const int level = *count;
+    __syncthreads();  // everyone has read the level before the next trip adds to it: one branch for the whole CTA
+    if (level > kCand - kStep * 8) {
+      const unsigned long long l = best_of(cand, level, lists, warp, lane);
       if (warp == 0) cand[lane] = l;
       if (tid == 0) *count = 32;
       __syncthreads();
