@@ -1,8 +1,8 @@
 """ctypes binding of libddt.so (C ABI in include/ddt.h).
 
 Argument marshalling only: tensors are checked for device, dtype, shape and
-contiguity, then their device pointers and the current CUDA stream go to the
-library. Every step of the tree-verify path runs in the library's kernels;
+contiguity, then their device pointers and the current CUDA stream (or the
+explicit one, which then owns what the call allocates) go to the library. Every step of the tree-verify path runs in the library's kernels;
 there is no Python or CPU fallback -- if libddt.so cannot be loaded, every
 call raises.
 """
@@ -185,6 +185,14 @@ def _device(*tensors, stream=None):
     if dev.index is None or dev.index == torch.cuda.current_device():
         return contextlib.nullcontext()
     return torch.cuda.device(dev)
+
+
+def _on(stream):
+    """The context in which a call allocates what its caller did not bring: the
+    explicit stream, if any, owns it. A block of the current stream's could be
+    handed out again while the explicit stream still uses it, and its fill
+    would not be ordered before the kernels."""
+    return _SAME_DEVICE if stream is None else torch.cuda.stream(stream)
 
 
 _F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
@@ -661,19 +669,21 @@ def cache_evict(kv: torch.Tensor, score: torch.Tensor, cache_off: torch.Tensor, 
         if not isinstance(d_kv, torch.Tensor) or d_kv.dim() != 2 or d_kv.shape[1] != row_elems:
             raise ValueError("dst[kv]: expected [rows, row_elems]")
         d_rows = d_kv.shape[0]
-    if out is None:
-        if max_keep is None:
-            max_keep = max(1, int(max_cache_len))
-        out = {"src": torch.empty(n_layers, B, max_keep, dtype=_I32, device=kv.device)}
-    if "new_len" not in out:
-        out["new_len"] = cache_len if dst is None else torch.empty_like(cache_len)
+    with _on(stream):
+        if out is None:
+            if max_keep is None:
+                max_keep = max(1, int(max_cache_len))
+            out = {"src": torch.empty(n_layers, B, max_keep, dtype=_I32, device=kv.device)}
+        if "new_len" not in out:
+            out["new_len"] = cache_len if dst is None else torch.empty_like(cache_len)
+        if workspace is None:
+            workspace = torch.empty(cache_evict_workspace_size(B, n_layers, max_cache_len), dtype=torch.uint8,
+                                    device=kv.device)
     if "src" not in out or out["src"].dim() != 3:
         raise ValueError("out: missing src [n_layers, B, max_keep]")
     src, new_len = out["src"], out["new_len"]
     if max_keep is None:
         max_keep = src.shape[2]
-    if workspace is None:
-        workspace = torch.empty(cache_evict_workspace_size(B, n_layers, max_cache_len), dtype=torch.uint8, device=kv.device)
     b, r, lbk = (B,), (rows,), (n_layers, B, max_keep)
     try:
         fits = (_fits(score, _F32, r, dev) and _fits(cache_off, _I64, b, dev) and _fits(cache_len, _I32, b, dev) and

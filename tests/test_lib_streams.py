@@ -1,0 +1,124 @@
+"""Calls with an explicit stream: what the binding allocates for them belongs
+to that stream, so that the caching allocator neither hands out a block that
+the stream still uses nor gives it one whose fill it does not wait for. On the
+CPU the library is a stub and the allocations are watched; on a GPU the calls
+run late on a side stream while the current one takes and fills memory."""
+import contextlib
+import types
+
+import numpy as np
+import pytest
+import torch
+from torch.overrides import TorchFunctionMode
+
+from ddtree_speculative_decode_b200 import lib
+
+DEV = "cuda:0"
+gpu = pytest.mark.gpu
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that passes for one on a GPU."""
+
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+def t(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+
+I32, I64, BF = torch.int32, torch.int64, torch.bfloat16
+
+
+def ints(n, dtype=I32):
+    return t(n, dtype=dtype)
+
+
+def evict():
+    a = (t(64, 8), t(64), ints(2, I64), ints(2), ints(2), 1, 1, 16)
+    return lambda **kw: lib.cache_evict(*a, **kw)
+
+
+def evict_into():
+    a = (t(64, 8), t(64), ints(2, I64), ints(2), ints(2), 1, 1, 16)
+    dst = {"kv": t(32, 8), "score": t(32), "off": ints(2, I64)}
+    return lambda **kw: lib.cache_evict(*a, dst=dst, **kw)
+
+
+CALLS = [evict, evict_into]
+
+
+@pytest.mark.parametrize("make", CALLS, ids=lambda c: c.__name__)
+def test_allocations_belong_to_the_stream(make, monkeypatch):
+    call = make()
+    active, seen = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, active[0] = active[0], stream
+        yield
+        active[0] = before
+
+    class Watch(TorchFunctionMode):
+        def __torch_function__(self, func, types, args=(), kwargs=None):
+            if func in (torch.empty, torch.zeros, torch.empty_like, torch.zeros_like, torch.full):
+                seen.append(active[0])
+            return func(*args, **(kwargs or {}))
+
+    class Stub:
+        def __getattr__(self, name):
+            return (lambda *a: 512) if name.endswith("_size") else (lambda *a: lib.DDT_OK)
+
+    monkeypatch.setattr(lib, "load", lambda: Stub())
+    monkeypatch.setattr(lib, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(lib, "_device", lambda *a, **k: contextlib.nullcontext())
+    monkeypatch.setattr(lib, "_ready", lambda *a: False)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    side = types.SimpleNamespace(cuda_stream=7, device=torch.device("cpu"))
+    with Watch():
+        call(stream=side)
+    assert seen and all(s is side for s in seen)
+
+
+def late(side):
+    """Keeps a stream busy for some milliseconds."""
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+
+
+def take_and_fill(sizes, value, times=40):
+    """Takes blocks of these sizes from the current stream's memory and fills them, again and again."""
+    for _ in range(times):
+        for n in sizes:
+            torch.full((n,), value, dtype=torch.uint8, device=DEV)
+
+
+@gpu
+def test_evict_on_a_side_stream():
+    layers, L, keep = 16, 6000, 2500
+    g = torch.Generator(device=DEV).manual_seed(1)
+    kv, score = torch.randn(layers * L, 80, device=DEV, generator=g), torch.rand(layers * L, device=DEV, generator=g)
+    off = torch.zeros(1, dtype=I64, device=DEV)
+    n, k = torch.tensor([L], dtype=I32, device=DEV), torch.tensor([keep], dtype=I32, device=DEV)
+    size = lib.cache_evict_workspace_size(1, layers, L)
+    side = torch.cuda.Stream()
+    for dst in (None, {"kv": torch.zeros(layers * keep, 80, device=DEV), "score": torch.zeros(layers * keep, device=DEV),
+                       "off": off, "layer_stride_rows": keep}):
+        x, s, c = kv.clone(), score.clone(), n.clone()
+        late(side)
+        out = lib.cache_evict(x, s, off, c, k, 4, 100, L, n_layers=layers, layer_stride_rows=L, dst=dst, stream=side)
+        take_and_fill([size, layers * L * 4], 0x7f)
+        torch.cuda.synchronize()
+        assert out["new_len"].tolist() == [keep]
+        order = score.view(layers, L).clone()
+        order[:, :4] = np.inf
+        order[:, L - 100:] = np.inf
+        want = order.sort(dim=-1, descending=True, stable=True).indices[:, :keep].sort(-1).values
+        assert torch.equal(out["src"][:, 0, :keep].long(), want)
+        rows, step = (x, L) if dst is None else (dst["kv"], keep)
+        for la in range(layers):
+            assert torch.equal(rows[la * step:la * step + keep], kv[la * L + want[la]])
