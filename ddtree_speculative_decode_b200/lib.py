@@ -593,7 +593,8 @@ def cache_weights(q: torch.Tensor, lse: torch.Tensor, kv: torch.Tensor, score: t
     if workspace is None:
         need = cache_weights_workspace_size(B, M if nodes is not None else N, H, d, int(max_cache_len), q.dtype)
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+            with _on(stream):
+                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     b, r = (B,), (rows,)
     try:
         fits = (_fits(lse, _F32, (B, N, H), dev) and _fits(kv, q.dtype, (rows, d), dev) and _fits(score, _F32, r, dev) and

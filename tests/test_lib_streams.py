@@ -48,7 +48,12 @@ def evict_into():
     return lambda **kw: lib.cache_evict(*a, dst=dst, **kw)
 
 
-CALLS = [evict, evict_into]
+def weights():
+    a = (t(2, 3, 4, 64, dtype=BF), t(2, 3, 4), t(64, 64, dtype=BF), t(64), ints(2, I64), ints(2), ints(2), 0.1, 16)
+    return lambda **kw: lib.cache_weights(*a, **kw)
+
+
+CALLS = [evict, evict_into, weights]
 
 
 @pytest.mark.parametrize("make", CALLS, ids=lambda c: c.__name__)
@@ -122,3 +127,27 @@ def test_evict_on_a_side_stream():
         rows, step = (x, L) if dst is None else (dst["kv"], keep)
         for la in range(layers):
             assert torch.equal(rows[la * step:la * step + keep], kv[la * L + want[la]])
+
+
+@gpu
+@pytest.mark.parametrize("busy", ["side", "current"])
+def test_weights_on_a_side_stream(busy):
+    """A workspace whose zeros come late, or are overwritten early, holds a status or counts that are none."""
+    L, H, d = 3000, 64, 576
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q, kv = torch.randn(1, 24, H, d, device=DEV, generator=g).bfloat16(), torch.randn(L, d, device=DEV, generator=g).bfloat16()
+    lse = torch.full((1, 24, H), 60.0, device=DEV)
+    off = torch.zeros(1, dtype=I64, device=DEV)
+    cl, n = torch.tensor([L], dtype=I32, device=DEV), torch.tensor([24], dtype=I32, device=DEV)
+    want, score = torch.zeros(L, device=DEV), torch.zeros(L, device=DEV)
+    lib.cache_weights(q, lse, kv, want, off, cl, n, 0.04, L)
+    size = lib.cache_weights_workspace_size(1, 24, H, d, L, BF)
+    side = torch.cuda.Stream()
+    status = torch.full((1,), 9, dtype=I32, device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    take_and_fill([size], 0x7f, 1)  # what a block of that size holds
+    late(side) if busy == "side" else torch.cuda._sleep(20_000_000)
+    lib.cache_weights(q, lse, kv, score, off, cl, n, 0.04, L, status=status, stream=side)
+    take_and_fill([size], 0x7f)
+    torch.cuda.synchronize()
+    assert status.tolist() == [lib.DDT_OK] and torch.equal(score, want)
