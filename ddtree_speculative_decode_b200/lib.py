@@ -246,9 +246,10 @@ def drafter_topk(logits: torch.Tensor, K: int, out: Optional[dict] = None, strea
         R *= d
     dev = logits.device
     if out is None:
-        out = {"logp": torch.empty(*lead, K, dtype=torch.float32, device=dev),
-               "tok": torch.empty(*lead, K, dtype=torch.int32, device=dev),
-               "status": torch.empty(*lead, dtype=torch.int32, device=dev)}
+        with _on(stream):
+            out = {"logp": torch.empty(*lead, K, dtype=torch.float32, device=dev),
+                   "tok": torch.empty(*lead, K, dtype=torch.int32, device=dev),
+                   "status": torch.empty(*lead, dtype=torch.int32, device=dev)}
     _check_out(out, {"logp": (torch.float32, lead + (K,)), "tok": (torch.int32, lead + (K,)),
                      "status": (torch.int32, lead)})
     with _device(logits, *out.values(), stream=stream):
@@ -271,7 +272,8 @@ def build_tree(logp: torch.Tensor, tok: torch.Tensor, root_tok: torch.Tensor, ca
     dev = logp.device
     W = (N + 31) // 32
     if out is None:
-        out = alloc_tree(B, N, dev)
+        with _on(stream):
+            out = alloc_tree(B, N, dev)
     i32 = torch.int32
     _check_out(out, {"node_tok": (i32, (B, N)), "parent": (i32, (B, N)), "depth": (i32, (B, N)),
                      "pos": (i32, (B, N)), "score": (torch.float32, (B, N)), "mask": (i32, (B, N, W)),
@@ -330,18 +332,19 @@ def verify_attn(q: torch.Tensor, kv: torch.Tensor, cache_off: torch.Tensor, cach
     _check(mask, "mask", torch.int32, (B, N, (N + 31) // 32))
     _check(n_nodes, "n_nodes", torch.int32, (B,))
     odt = out_dtype or q.dtype
-    if out is None:
-        out = torch.empty(B, N, H, d_l, dtype=odt, device=q.device)
+    need = verify_attn_workspace_size(B, N, H, d_l, d_r, max_cache_len, q.dtype)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(B, N, H, d_l, dtype=odt, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty(B, N, H, dtype=torch.float32, device=q.device)
+        if workspace is None and need > 0:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)  # status word must start at 0
     _check(out, "out", odt, (B, N, H, d_l))
-    if lse is None and want_lse:
-        lse = torch.empty(B, N, H, dtype=torch.float32, device=q.device)
     if lse is not None:
         _check(lse, "lse", torch.float32, (B, N, H))
     if status is not None:
         _check(status, "status", torch.int32, (B,))
-    need = verify_attn_workspace_size(B, N, H, d_l, d_r, max_cache_len, q.dtype)
-    if workspace is None and need > 0:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)  # status word must start at 0
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with _device(q, kv, cache_off, cache_len, mask, n_nodes, out, lse, status, workspace, stream=stream):
         st = load().ddt_verify_attn(_ptr(q), _ptr(kv), kv.shape[0], _ptr(cache_off), _ptr(cache_len), _ptr(mask),
@@ -373,12 +376,13 @@ def accept_compact(logits: torch.Tensor, node_tok: torch.Tensor, parent: torch.T
     _check(cache_len, "cache_len", torch.int32, (B,))
     _check(cache_cap, "cache_cap", torch.int32, (B,))
     dev = logits.device
-    if out is None:
-        out = alloc_accept(B, N, dev)
-    _check_out(out, _accept_out_spec(B, N))
     need = accept_compact_workspace_size(B, N, V)
-    if workspace is None:
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)  # arrival counters start at 0
+    with _on(stream):
+        if out is None:
+            out = alloc_accept(B, N, dev)
+        if workspace is None:
+            workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)  # arrival counters start at 0
+    _check_out(out, _accept_out_spec(B, N))
     _check(workspace, "workspace", None)
     row_elems = kv.shape[-1]
     with _device(logits, node_tok, parent, n_nodes, kv, cache_off, cache_len, cache_cap,
@@ -424,7 +428,8 @@ def accept_compact_noalloc(logits: torch.Tensor, node_tok: torch.Tensor, parent:
     _check(cache_len, "cache_len", torch.int32, (B,))
     _check(cache_cap, "cache_cap", torch.int32, (B,))
     if out is None:
-        out = alloc_accept(B, N, logits.device)
+        with _on(stream):
+            out = alloc_accept(B, N, logits.device)
     _check_out(out, _accept_out_spec(B, N))
     with _device(logits, node_tok, parent, n_nodes, kv, cache_off, cache_len, cache_cap,
                  *out.values(), stream=stream):
@@ -459,12 +464,13 @@ def accept_compact_lmhead(hidden: torch.Tensor, w_vocab: torch.Tensor, node_tok:
     _check(cache_len, "cache_len", torch.int32, (B,))
     _check(cache_cap, "cache_cap", torch.int32, (B,))
     dev = hidden.device
-    if out is None:
-        out = alloc_accept(B, N, dev)
-    _check_out(out, _accept_out_spec(B, N))
     need = accept_compact_workspace_size(B, N, V)
-    if workspace is None:
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)  # row keys start at 0
+    with _on(stream):
+        if out is None:
+            out = alloc_accept(B, N, dev)
+        if workspace is None:
+            workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)  # row keys start at 0
+    _check_out(out, _accept_out_spec(B, N))
     _check(workspace, "workspace", None)
     row_elems = kv.shape[-1]
     with _device(hidden, w_vocab, node_tok, parent, n_nodes, kv, cache_off, cache_len, cache_cap, workspace,
@@ -519,7 +525,8 @@ def token_logprobs(logits: torch.Tensor, tok: torch.Tensor, nodes: Optional[torc
     M = tok.shape[1]
     dev = logits.get_device()
     if out is None and dev >= 0:
-        out = alloc_logprobs(B, M, K, logits.device)
+        with _on(stream):
+            out = alloc_logprobs(B, M, K, logits.device)
     bm, bmk = (B, M), (B, M, K)
     try:
         logp, entropy, top_logp, top_tok, status = out["logp"], out["entropy"], out["top_logp"], out["top_tok"], out["status"]

@@ -33,8 +33,8 @@ def t(*shape, dtype=torch.float32):
 I32, I64, BF = torch.int32, torch.int64, torch.bfloat16
 
 
-def ints(n, dtype=I32):
-    return t(n, dtype=dtype)
+def ints(shape, dtype=I32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
 
 
 def evict():
@@ -53,7 +53,43 @@ def weights():
     return lambda **kw: lib.cache_weights(*a, **kw)
 
 
-CALLS = [evict, evict_into, weights]
+def logprobs():
+    a = (t(2, 3, 50), ints((2, 3)))
+    return lambda **kw: lib.token_logprobs(*a, K=4, **kw)
+
+
+def topk():
+    a = (t(2, 3, 50), 4)
+    return lambda **kw: lib.drafter_topk(*a, **kw)
+
+
+def tree():
+    a = (t(2, 3, 4), ints((2, 3, 4)), ints(2), ints(2), 8)
+    return lambda **kw: lib.build_tree(*a, **kw)
+
+
+def attention():
+    a = (t(2, 8, 4, 80), t(64, 80), ints(2, I64), ints(2), ints((2, 8, 1)), ints(2), 64, 16, 0.1, 16)
+    return lambda **kw: lib.verify_attn(*a, **kw)
+
+
+def accept():
+    a = (t(2, 8, 50), ints((2, 8)), ints((2, 8)), ints(2), t(64, 80), ints(2, I64), ints(2), ints(2))
+    return lambda **kw: lib.accept_compact(*a, **kw)
+
+
+def accept_noalloc():
+    a = (t(2, 8, 50), ints((2, 8)), ints((2, 8)), ints(2), t(64, 80), ints(2, I64), ints(2), ints(2))
+    return lambda **kw: lib.accept_compact_noalloc(*a, **kw)
+
+
+def accept_lmhead():
+    a = (t(2, 8, 64, dtype=BF), t(50, 64, dtype=BF), ints((2, 8)), ints((2, 8)), ints(2), t(64, 80), ints(2, I64), ints(2),
+         ints(2))
+    return lambda **kw: lib.accept_compact_lmhead(*a, **kw)
+
+
+CALLS = [evict, evict_into, weights, logprobs, topk, tree, attention, accept, accept_noalloc, accept_lmhead]
 
 
 @pytest.mark.parametrize("make", CALLS, ids=lambda c: c.__name__)
@@ -151,3 +187,62 @@ def test_weights_on_a_side_stream(busy):
     take_and_fill([size], 0x7f)
     torch.cuda.synchronize()
     assert status.tolist() == [lib.DDT_OK] and torch.equal(score, want)
+
+
+@gpu
+@pytest.mark.parametrize("busy", ["side", "current"])
+def test_a_step_on_a_side_stream(busy):
+    """Top-k, attention, accept and token log-probs on a stream of their own, without workspaces or outputs."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    B, N, H, V, L = 2, 24, 64, 3001, 500
+    draft = torch.randn(B, 6, V, device=DEV, generator=g)
+    root, cl = torch.tensor([1, 2], dtype=I32, device=DEV), torch.tensor([L, L - 100], dtype=I32, device=DEV)
+    off, cap = torch.tensor([0, 700], dtype=I64, device=DEV), torch.tensor([700, 700], dtype=I32, device=DEV)
+    q, kv = (torch.randn(*s, device=DEV, generator=g).bfloat16() for s in ((B, N, H, 576), (1400, 576)))
+    logits = torch.randn(B, N, V, device=DEV, generator=g)
+    hidden, head = (torch.randn(*s, device=DEV, generator=g).bfloat16() for s in ((B, N, 512), (V, 512)))
+
+    def step(stream):
+        def between():
+            if stream is not None:
+                late(stream) if busy == "side" else torch.cuda._sleep(20_000_000)
+
+        def take():
+            if stream is not None:
+                take_and_fill([256, lib.verify_attn_workspace_size(B, N, H, 512, 64, 4 * L, BF),
+                               lib.accept_compact_workspace_size(B, N, V)], 0x7f)
+
+        pools, lens, outs = [kv.clone(), kv.clone()], [cl.clone(), cl.clone()], []
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        between()
+        top = lib.drafter_topk(draft, 4, stream=stream)
+        take()
+        between()
+        tr = lib.build_tree(top["logp"], top["tok"], root, cl, N, stream=stream)
+        take()
+        between()
+        o = lib.verify_attn(q, kv, off, cl, tr["mask"], tr["n_nodes"], 512, 64, 0.04, 4 * L, stream=stream)
+        take()
+        between()
+        a = lib.accept_compact(logits, tr["node_tok"], tr["parent"], tr["n_nodes"], pools[0], off, lens[0], cap, stream=stream)
+        take()
+        between()
+        h = lib.accept_compact_lmhead(hidden, head, tr["node_tok"], tr["parent"], tr["n_nodes"], pools[1], off, lens[1], cap,
+                                      stream=stream)
+        take()
+        between()
+        lp = lib.token_logprobs(logits, a["out_tok"], nodes=a["acc_nodes"], K=3, stream=stream)
+        take()
+        torch.cuda.synchronize()
+        for d in (top, tr, a, h, lp, dict(enumerate(pools + lens))):
+            outs += [v.clone() for v in d.values()]
+        return o, outs
+
+    (o0, l0), want = step(None)
+    (o1, l1), got = step(torch.cuda.Stream())
+    assert len(want) == len(got) and [i for i, (a, b) in enumerate(zip(want, got)) if not torch.equal(a, b)] == []
+    # the attention joins its parts in the order in which they end: float32 sums of at most 32 parts of values below 6
+    # in another order (2 x 32 x 2^-24 x 6 = 2.3e-5), each rounded to bf16 (half a step, 2^-8, on both sides)
+    assert bool(((o0.float() - o1.float()).abs() <= 2.0 ** -7 * o0.float().abs() + 2.3e-5).all())
+    assert bool(((l0 - l1).abs() <= 2.3e-5).all())
