@@ -75,6 +75,7 @@ constexpr int kFew = 8;           // up to this many alternatives the warps' bou
 constexpr int kPick = 128;        // keys that reach the bound
 constexpr float kFar = -150.0f;   // e^kFar and 2^kFar are zero in float32
 constexpr float kUsual = 1e6f;    // below this, a logit in base 2 is off by less than one before it is rounded
+constexpr float kUsualTop = 999999.9375f;  // the largest float below kUsual
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kAhead = 16.0f;   // base-2 exponents may exceed the reference by this much
 
@@ -759,7 +760,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
             limit = M;
             if (fabsf(M) < kUsual) {  // -> base 2 relative to the new ref
               ref = ceilf(M * kLog2e);
-              limit = (ref + kAhead) * kLn2;
+              // no further than the usual logits: what passes it changes the sums' form here
+              limit = fminf((ref + kAhead) * kLn2, kUsualTop);
               k = fmaf(M, kLog2e, -ref);
               e = ex2_ftz(k);
               u2 = mul2(fma2(u2, pack2(kLog2e, kLog2e), mul2(pack2(k, k), s2)), pack2(e, e));
