@@ -531,11 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the key's parts, then the shares
       s.sums[h][row] = sum;
-      named_bar_sync(1, 256);
+      // one wait that gave up spoils the CTA's item: a key's parts come from
+      // two warps, a share's from eight
+      const bool good = bar_red_and(1, 256, ok);
       if (et < kKeys) {  // whose row is et: key0 + et
         const int key = key0 + et;
         sum = s.sums[0][et] + s.sums[1][et];
-        bool write = ok;
+        bool write = good;
         if (nshare > 1) {
           const int part = s.tile0[cur.b] + kt;
           float* mine = p.parts + ((int64_t)part * s.shares) * kTile + kKeys * (int)rank + et;
@@ -547,12 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // their reading
             unsigned* cnt = p.counters + 2 * part + rank;
             unsigned old_count = 0u;
-            if (ok) asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(old_count) : "l"(cnt) : "memory");
-            s.last = ok && old_count == (unsigned)nshare - 1u;
+            if (good) asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(old_count) : "l"(cnt) : "memory");
+            s.last = good && old_count == (unsigned)nshare - 1u;
             if (s.last) *cnt = 0u;
           }
           named_bar_sync(2, kKeys);
-          write = ok && *reinterpret_cast<volatile int*>(&s.last) != 0;
+          write = good && *reinterpret_cast<volatile int*>(&s.last) != 0;
           if (write) {
             sum = 0.0f;
 #pragma unroll

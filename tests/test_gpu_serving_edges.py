@@ -51,3 +51,35 @@ def test_logits_around_a_million(K, dtype):
     logits = torch.stack(rows).to(dtype)[None]
     tok = torch.tensor([[100, 100 + step] * (len(rows) // 2)])
     check(logits, tok, K=K)
+
+
+@gpu
+@pytest.mark.parametrize("lens,N,H", [([700, 90], 1, 64), ([700, 90], 40, 64), ([300] * 3, 5, 8)])
+def test_weights_workspace_that_holds_a_timeout(lens, N, H):
+    """No work until the workspace is zeroed: the status of every request, no score touched, then the scores of a call
+    with a fresh workspace, bit for bit. One, several and no shares of the query rows."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    B, rows = len(lens), sum(lens)
+    q, kv = (torch.randn(*s, device=DEV, generator=g).bfloat16() for s in ((B, N, H, 576), (rows, 576)))
+    lse, prev = torch.full((B, N, H), 30.0, device=DEV), torch.rand(rows, device=DEV, generator=g)
+    off = torch.tensor([sum(lens[:b]) for b in range(B)], device=DEV)
+    cl, n = torch.tensor(lens, **i32), torch.tensor([N] * B, **i32)
+    ws = torch.zeros(lib.cache_weights_workspace_size(B, N, H, 576, max(lens), torch.bfloat16), dtype=torch.uint8, device=DEV)
+
+    def call(ws):
+        score, status = prev.clone(), torch.full((B,), 9, **i32)
+        lib.cache_weights(q, lse, kv, score, off, cl, n, 0.04, max(lens), prev=score, decay=0.5, status=status, workspace=ws)
+        return score, status.tolist()
+
+    want, status = call(None)
+    assert status == [lib.DDT_OK] * B and not torch.equal(want, prev)
+    ws[:4].view(torch.int32)[0] = lib.DDT_ERR_TIMEOUT
+    for _ in range(2):
+        score, status = call(ws)
+        assert status == [lib.DDT_ERR_TIMEOUT] * B and torch.equal(score, prev)
+    assert int(ws[:4].view(torch.int32)[0]) == lib.DDT_ERR_TIMEOUT and not bool(ws[4:].any())
+    ws.zero_()
+    score, status = call(ws)
+    assert status == [lib.DDT_OK] * B and torch.equal(score, want)
+    assert not bool(ws[:256].any())
