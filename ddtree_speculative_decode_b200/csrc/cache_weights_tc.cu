@@ -61,6 +61,7 @@ constexpr int kSlabBytes = kKeys * 128;  // 128 keys x 64 dims bf16
 constexpr int kMaxB = 256;           // requests of one launch
 constexpr int kMaxShares = 16;
 constexpr int kMaxParts = 320;       // (key tile, share) partials of a split launch
+constexpr uint64_t kLandNs = 100000; // pause before leaving when a wait gave up
 
 constexpr int kBarAFull = 0;                          // [kMaxSlabs] leader: a stage's keys (both CTAs)
 constexpr int kBarBFull = kBarAFull + kMaxSlabs;      // [kMaxStages] leader: a stage of query rows
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
   const bool aborted = *reinterpret_cast<volatile int*>(&s.aborted) != 0;
 
+  bool ok = true;  // no wait of this thread gave up
   if (aborted) {
     // straight to the teardown
   } else if (warp == 0) {
@@ -319,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t afull0 = map_to_rank(bar(kBarAFull), 0), bfull0 = map_to_rank(bar(kBarBFull), 0);
     int slot = 0, issued = 0;
     uint32_t phase = 0;
-    bool ok = true;
     Cursor cur(pair);
     int kt, share, nshare, u0, u1, per;
     bool ahead = true;  // the first item's keys need no wait: all their loads go first
@@ -383,22 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ahead = false;
     }
-    if (!ok) {
-      // a wait gave up: let the copies in flight land (bounded) before the
-      // CTAs leave; the leader's barriers count both CTAs' bytes
-      if (leader && lane == 0)
-        for (int i = 0; i < p.stages && i < issued; ++i) {
-          const int q = issued - 1 - i;
-          (void)mbar_wait_own(bar(kBarBFull + q % p.stages), (uint32_t)((q / p.stages) & 1), abort, wlim);
-        }
-      const uint64_t t = global_timer_ns();
-      while (global_timer_ns() - t < 100000) __nanosleep(1000);
-    }
   } else if (warp == 1 && lane == 0 && leader) {
     // ============================================================ MMA issuer
     int slot = 0, at = 0;
     uint32_t phase = 0, aphase = 0;
-    bool ok = true;
     Cursor cur(pair);
     int kt, share, nshare, u0, u1, per;
     for (; ok && cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
@@ -450,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t empty0 = map_to_rank(bar(kBarAccEmpty), 0);
     const int row = 32 * q + lane;
     int at = 0;
-    bool ok = true;
     Cursor cur(pair);
     int kt, share, nshare, u0, u1, per;
     for (; cur.get(s, p, kt, share, nshare, u0, u1, per); cur.item += npairs) {
@@ -568,7 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {
+    // Copies and MMAs that nobody waited for may be in flight: every role of
+    // this CTA has issued its last ones, and they take a few microseconds. The
+    // pair leaves together, so one CTA's pause is both's.
+    const uint64_t t = global_timer_ns();
+    while (global_timer_ns() - t < kLandNs) __nanosleep(1000);
+    __syncwarp();
+  }
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();

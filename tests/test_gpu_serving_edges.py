@@ -83,3 +83,44 @@ def test_weights_workspace_that_holds_a_timeout(lens, N, H):
     score, status = call(ws)
     assert status == [lib.DDT_OK] * B and torch.equal(score, want)
     assert not bool(ws[:256].any())
+
+
+@gpu
+@pytest.mark.parametrize("lens,N", [([16384] * 4, 64), ([4096], 64), ([9000] * 60, 1)])
+def test_weights_status_word_set_at_any_time(lens, N):
+    """The status word is set from another stream before, while and after the kernel runs (waits look at it only when
+    they last long). Every score is then either untouched or the right one, bit for bit, and the workspace works again
+    once it is zeroed."""
+    H, B, rows = 64, len(lens), sum(lens)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    q, kv = (torch.randn(*s, device=DEV, generator=g).bfloat16() for s in ((B, N, H, 576), (rows, 576)))
+    lse, prev = torch.full((B, N, H), 30.0, device=DEV), torch.rand(rows, device=DEV, generator=g)
+    off = torch.tensor([sum(lens[:b]) for b in range(B)], device=DEV)
+    cl, n = torch.tensor(lens, **i32), torch.tensor([N] * B, **i32)
+    ws = torch.zeros(lib.cache_weights_workspace_size(B, N, H, 576, max(lens), torch.bfloat16), dtype=torch.uint8, device=DEV)
+    word = ws[:4].view(torch.int32)
+
+    def call(score):
+        lib.cache_weights(q, lse, kv, score, off, cl, n, 0.04, max(lens), prev=score, decay=0.5, workspace=ws)
+
+    want = prev.clone()
+    call(want)
+    assert not bool((want == prev).any())
+    # the call behind a spin of `ahead` cycles, the word behind others: before, during and after the kernel
+    side, ahead = torch.cuda.Stream(), 2_000_000
+    for k in range(16):
+        score = prev.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(ahead)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(ahead + 20_000 * (k - 5))
+            word.fill_(lib.DDT_ERR_TIMEOUT)
+        call(score)
+        torch.cuda.synchronize()
+        done = score == want
+        assert bool((done | (score == prev)).all())
+        ws.zero_()
+        again = prev.clone()
+        call(again)
+        assert torch.equal(again, want)
