@@ -130,16 +130,21 @@ class TinyMLAEngine:
             return
         L = self.length
         cl = self._i32(L)
+        status = torch.zeros((self.n_layers, 1), dtype=torch.int32, device=self.dev)
         for li, (q, lse) in enumerate(self.seen):
             score = self.score[li * self.stride:(li + 1) * self.stride]
             score[L - new:L] = 0.0
             lib.cache_weights(q, lse, self.layer(li), score, self.off, cl, self._i32(q.shape[1]), self.scale, L,
-                              nodes=nodes, causal=True, prev=score, decay=self.decay)
+                              nodes=nodes, causal=True, prev=score, decay=self.decay, status=status[li])
+        if int(status.max().item()) != lib.DDT_OK:
+            raise RuntimeError("cache weights reported an error")
         if L > self.budget:
             lib.cache_evict(self.kv, self.score, self.off, cl, self._i32(self.budget), self.sink, self.recent, L,
-                            n_layers=self.n_layers, layer_stride_rows=self.stride)
-            self.evicted += L - self.budget
-            self.length = self.budget
+                            n_layers=self.n_layers, layer_stride_rows=self.stride, status=status[0])
+            if int(status[0].item()) != lib.DDT_OK:
+                raise RuntimeError("cache eviction reported an error")
+            self.length = int(cl[0].item())
+            self.evicted += L - self.length
 
     def _one_row(self, tok: int) -> int:
         toks = torch.tensor([int(tok)], dtype=torch.int64, device=self.dev)

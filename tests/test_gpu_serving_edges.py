@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from ddtree_speculative_decode_b200 import lib
+from ddtree_speculative_decode_b200 import lib, spec_engine, synth
 from test_gpu_logprobs import check
 
 DEV = "cuda:0"
@@ -124,3 +124,24 @@ def test_weights_status_word_set_at_any_time(lens, N):
         again = prev.clone()
         call(again)
         assert torch.equal(again, want)
+
+
+@gpu
+@pytest.mark.parametrize("name,index,value", [("cache_weights", 6, -1), ("cache_evict", 4, -1)])
+def test_engine_notices_a_skipped_call(name, index, value, monkeypatch):
+    """A request that the device skips (here: for a negative count) raises; the engine's length stays the cache's."""
+    real = getattr(lib, name)
+    eng = spec_engine.TinyMLAEngine(synth.tiny_mla_weights(), 64, cache_budget=4, sink=1, recent=1)
+    for t in (3, 14, 15, 92):
+        eng._one_row(t)
+    kv, score = eng.kv.clone(), eng.score.clone()
+    monkeypatch.setattr(lib, name, lambda *a, **k: real(*a[:index], torch.full_like(a[index], value), *a[index + 1:], **k))
+    with pytest.raises(RuntimeError, match="error"):
+        eng._one_row(65)
+    assert eng.length == 5 and eng.evicted == 0
+    for la in range(eng.n_layers):
+        rows = slice(la * eng.stride, la * eng.stride + 4)
+        assert torch.equal(eng.kv[rows], kv[rows])
+        if name == "cache_weights":
+            assert torch.equal(eng.score[rows], score[rows])
+    monkeypatch.setattr(lib, name, real)
