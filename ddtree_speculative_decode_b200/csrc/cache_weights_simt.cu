@@ -208,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, 2) cache_weights_simt_kernel(Weights
 template <typename T, int KP, int RP>
 static int launch_tile(WeightsParams p, int max_cache_len, cudaStream_t stream) {
   constexpr int kKeys = 16 * KP;
+  // a request's tiles, as far as the grid allows: a CTA takes every p.tiles-th
   p.tiles = std::max(1, max_cache_len / kKeys + (max_cache_len % kKeys != 0 ? 1 : 0));
-  const long long grid = (long long)p.tiles * p.B;
-  if (grid > 0x7fffffffLL) return DDT_ERR_UNSUPPORTED;
-  return launch_pdl(cache_weights_simt_kernel<T, KP, RP>, (unsigned)grid, kThreads, 0, stream, p);
+  p.tiles = std::min(p.tiles, 0x7fffffff / p.B);
+  return launch_pdl(cache_weights_simt_kernel<T, KP, RP>, (unsigned)(p.tiles * p.B), kThreads, 0, stream, p);
 }
 template <typename T>
 static int launch_type(const WeightsParams& p, int max_cache_len, cudaStream_t stream) {

@@ -659,7 +659,7 @@ static int launch(Params p, int max_cache_len, cudaStream_t stream) {
   for (p.b0 = 0; p.b0 < w.B; p.b0 += kMaxB) {
     p.nb = std::min(kMaxB, w.B - p.b0);
     // every pair that could get an item, counting shares
-    const long long tiles = std::max(1LL, (long long)p.nb * ((max_cache_len + kTile - 1) / kTile));
+    const long long tiles = std::max(1LL, (long long)p.nb * (max_cache_len / kTile + (max_cache_len % kTile != 0 ? 1 : 0)));
     const long long items = tiles * std::min<long long>(kMaxShares, std::max(1LL, (long long)w.M * p.chunks));
     const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, items);
     cudaLaunchConfig_t cfg = {};

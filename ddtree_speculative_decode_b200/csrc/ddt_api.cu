@@ -1,6 +1,7 @@
 // C ABI entry points of libddt.so: host-side argument checks and dispatch to
 // the CUDA kernels. Every check here is synchronous and launches nothing on
 // failure; see include/ddt.h for the contract of each call.
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 
@@ -134,6 +135,8 @@ int ddt_cache_weights(const void* q, const float* lse, const void* kv, int64_t k
   p.decay = decay;
   p.score = score;
   p.dev_status = dev_status;
+  // of speed only, and no request has more rows than the pool
+  max_cache_len = (int)std::min<int64_t>(max_cache_len, kv_rows);
   if (ddt::weights_tc_supported(d_qk, in_dtype, nullptr, nullptr)) {
     if (!workspace || !ddt::aligned(workspace, 256) || workspace_bytes < ddt::weights_tc_workspace_bytes())
       return DDT_ERR_INVALID_ARG;

@@ -145,3 +145,24 @@ def test_engine_notices_a_skipped_call(name, index, value, monkeypatch):
         if name == "cache_weights":
             assert torch.equal(eng.score[rows], score[rows])
     monkeypatch.setattr(lib, name, real)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,H,d", [(torch.float32, 2, 40), (torch.bfloat16, 8, 64)])
+@pytest.mark.parametrize("most", [2 ** 31 - 1, 2 ** 31 - 300])
+def test_weights_with_the_loosest_bound(most, dtype, H, d):
+    """max_cache_len only has to be a bound: any one gives the same scores, for many requests as well."""
+    B, L = 200, 150
+    g = torch.Generator(device=DEV).manual_seed(3)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    q, kv = (torch.randn(*s, device=DEV, generator=g).to(dtype) for s in ((B, 2, H, d), (B * L, d)))
+    lse = torch.full((B, 2, H), 8.0, device=DEV)
+    off = torch.arange(B, device=DEV) * L
+    cl, n = torch.randint(1, L + 1, (B,), generator=g, **i32), torch.full((B,), 2, **i32)
+    got = []
+    for m in (L, most):
+        status, score = torch.full((B,), 9, **i32), torch.full((B * L,), -7.0, device=DEV)
+        lib.cache_weights(q, lse, kv, score, off, cl, n, 0.1, m, status=status)
+        assert status.tolist() == [lib.DDT_OK] * B
+        got.append(score)
+    assert torch.equal(*got)
