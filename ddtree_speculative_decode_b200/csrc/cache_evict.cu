@@ -32,10 +32,13 @@
 // evicted one already lie in place and are left alone.
 //
 // Measured (bf16 rows of 576, half of the rows kept unless said; kernels only):
-//   1 x 4096 rows                 11 us, copy; 14 us in place (latency)
+//   1 x 4096 rows                 11 to 14 us, copy; 15 us in place (latency)
 //   1 x 32768 rows                21 us, copy; 50 us in place (few CTAs)
-//   61 layers of 4096 rows        57 us, copy (5.0 TB/s); 65 us in place
-//   16 layers of 4 x 32768 rows   405 us, copy (6.0 TB/s); 484 us in place
+//   61 layers of 4096 rows        58 us, copy (5.0 TB/s); 65 us in place
+//   16 layers of 4 x 32768 rows   405 to 416 us, copy (6.0 TB/s); 460 to 470 us in place
+// A few rows of a full cache, in place (nearly every row moves a few places):
+//   9 of 16393 rows, 61 layers    397 us (5.2 TB/s of rows that move); one layer 40 us
+//   9 of 16 x 4105, 61 layers     1454 us (5.8 TB/s)
 #include <algorithm>
 #include <mutex>
 

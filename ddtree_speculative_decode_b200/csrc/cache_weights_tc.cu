@@ -29,7 +29,9 @@
 // exponentials of a tile run under the next tile's MMAs.
 //
 // Bound: the tensor pipe for 4 and more nodes of 64 heads (256 x 256 x 576
-// per 4600 cycles; the exponentials take 2050), HBM for single tokens.
+// per 4600 cycles; the exponentials take 2050); the rounds of key tiles, the
+// plan and the drain for single tokens (16 requests of 1024 to 8192 rows: 313
+// tiles on 74 pairs, 20.5 us, 3.9 TB/s).
 //
 // Items are dealt to a persistent grid of pairs in order. With few key tiles
 // the query rows are split into S shares (the S of the shortest estimated

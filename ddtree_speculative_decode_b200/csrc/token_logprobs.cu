@@ -43,8 +43,11 @@
 //
 // Measured (bf16, rows of 163840; us): 512 rows 34.7 without alternatives, 45
 // with 8, 58 with 32; 2048 rows 111 without (6.0 TB/s), 136 with 8; 4096 rows
-// 244 with one (5.5 TB/s); instructions per logit 7.7 with none or one, 9.7
-// with 8, of which the row's end is the difference.
+// 244 to 274 with one (4.9 to 5.5 TB/s); instructions per logit 7.7 with none or
+// one, 9.7 with 8, of which the row's end is the difference. Constant rows, which
+// are all read again with care: one 84 (an ordinary one 9 with 1 or 8
+// alternatives), 64 136 (14), 512 700 (41 to 45); 512 rows of 300 distinct
+// values 400 to 440.
 #include <algorithm>
 #include <mutex>
 
@@ -468,6 +471,11 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(LogprobsPar
   int lc = p.log_share;  // log2 of C
   if (lc < 0) {
     lc = 0;
+    // Measured (163840 bf16 values a row; us with rows left over whole, in halves
+    // and in quarters): 512 rows (68 left) 45.1, 37.8, 34.3, with 8 alternatives
+    // 54.9, 47.6, 44.7; 600 rows (156 left) 46.0, 38.8, 40.6 and 55.4, 48.3, 56.2;
+    // 800 rows (356 left) 46.9, 50.1, 54.1 and 58.2, 65.5, 80.3. These
+    // constants choose the shortest of each.
     const int fixed = kTop ? 1500 : 500;
     float best = 0.0f;
     for (int l = 0; rest > 0 && (1 << l) <= csize; ++l) {
@@ -1066,6 +1074,15 @@ static int launch_t(LogprobsParams p, cudaStream_t stream) {
   // full waves if the rows fill the device; fewer rows are split so that one
   // wave of CTAs lies evenly on the SMs. One CTA alone keeps an SM about 45 %
   // busy, two 80 %.
+  // Measured, lists (163840 bf16 values a row; us in clusters of 8 and of 4):
+  // 2048 entries, 16 selected 10.6 and 11.4, 512 selected 45.5 and 37.4; 4096
+  // entries, 16 selected 11.3 and 12.3, 592 selected 55.7 and 43.5.
+  // All rows (us with 1, 2, 4 and 8 CTAs a row): 8 rows 11.1, 8.1, 6.1, 5.4; 32
+  // rows 11.6, 8.5, 7.2, 8.2; 64 rows 12.0, 8.9, 10.1; 100 rows 12.3, 11.9,
+  // 10.7; 148 rows 12.9, 15.3; 200 rows 17.9, 15.5. The estimate takes the
+  // last column: right at the ends, up to a fifth too slow between (32, 64, 148
+  // rows), two fifths for short rows with alternatives (48 rows of 32000 with 8:
+  // 12.6 with 8 CTAs a row, 8.8 with 2).
   int cluster = p.nodes && all <= 2048 ? kMaxC : 4;
   fit(cluster);
   p.log_share = -1;

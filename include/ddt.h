@@ -437,7 +437,9 @@ DDT_API int ddt_accept_compact_noalloc(const void* logits, int logits_dtype, int
  *   -inf / -1.
  * Sizes: B, N, M, V >= 1, 0 <= K <= min(V, 32), M <= N when nodes is null;
  *   B * M and B * N < 2^31 and V <= 2^30 (DDT_ERR_UNSUPPORTED beyond).
- * Every selected row is read once; rows that no entry selects are not read.
+ * Every selected row is read once (again, for K > 0, where more than 128 values
+ *   of a CTA's part reach the bound on its K best: rows of few distinct values,
+ *   which take up to 17 times as long); rows that no entry selects are not read.
  *   One launch (several for a node list of tens of thousands of entries); no workspace.
  *   Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, alignment),
  *   DDT_ERR_UNSUPPORTED, DDT_ERR_CUDA (launch).
@@ -488,9 +490,9 @@ DDT_API int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int6
  *   returns DDT_OK leaves what must be zero at zero. Its first word is a
  *   device status: waits inside the tensor-core kernel are bounded
  *   (ddt_set_wait_limit_ns), and one that expires stores DDT_ERR_TIMEOUT
- *   there; scores may then be missing, and later calls with that workspace do
- *   nothing until the caller zeroes it. Calls that share a workspace must not
- *   overlap in time.
+ *   there; scores may then be missing (never wrong), and later calls with that
+ *   workspace do nothing until the caller zeroes it. Calls that share a
+ *   workspace must not overlap in time.
  * Precondition the library cannot check: the requests own disjoint rows.
  * Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, scale not finite and
  *   positive, decay not finite, workspace), DDT_ERR_UNSUPPORTED (d_qk > 1024,
@@ -528,7 +530,8 @@ DDT_API int ddt_cache_weights(const void* q, const float* lse, const void* kv, i
  *   rows of the destination behind the kept ones are not written.
  *
  * Inputs (device): kv pool of kv_rows (host value: every layer's rows) rows
- *   of row_elems elements of kv_dtype (row size a multiple of 4 bytes);
+ *   of row_elems elements of kv_dtype (row size a multiple of 4 bytes, at
+ *   most 1 MB);
  *   score [kv_rows] float32, one per pool row (ddt_cache_weights writes
  *   them); cache_off [B] int64, cache_len [B] int32, keep [B] int32; dst_off
  *   [B] int64 and kv_dst pool of dst_rows rows with score_dst [dst_rows], or
