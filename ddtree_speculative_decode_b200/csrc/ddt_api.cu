@@ -17,6 +17,10 @@ static int bits_per_level(int K) {
 
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// rows and entries that the kernels count in 32 bits, and past the last one by
+// up to a launch's CTAs or a tile
+constexpr long long kMaxRows = (1LL << 31) - (1 << 16);
+
 static std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 
 uint64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
@@ -74,7 +78,7 @@ int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int64_t row_
   if (!nodes && M > N) return DDT_ERR_INVALID_ARG;
   if (logits_dtype != DDT_F32 && logits_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
   if (!ddt::aligned(logits, logits_dtype == DDT_F32 ? 4 : 2)) return DDT_ERR_INVALID_ARG;
-  if ((long long)B * M > 0x7fffffffLL || (long long)B * N > 0x7fffffffLL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
+  if ((long long)B * M >= ddt::kMaxRows || (long long)B * N > 0x7fffffffLL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
   ddt::LogprobsParams p{};
   p.logits = logits;
   p.logits_dtype = logits_dtype;

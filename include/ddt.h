@@ -436,7 +436,8 @@ DDT_API int ddt_accept_compact_noalloc(const void* logits, int logits_dtype, int
  *   +inf or no finite logit -- that entry gets logp -inf, entropy 0, top
  *   -inf / -1.
  * Sizes: B, N, M, V >= 1, 0 <= K <= min(V, 32), M <= N when nodes is null;
- *   B * M and B * N < 2^31 and V <= 2^30 (DDT_ERR_UNSUPPORTED beyond).
+ *   B * M < 2^31 - 2^16, B * N < 2^31 and V <= 2^30 (DDT_ERR_UNSUPPORTED
+ *   beyond).
  * Every selected row is read once (again, for K > 0, where more than 128 values
  *   of a CTA's part reach the bound on its K best: rows of few distinct values,
  *   which take up to 17 times as long); rows that no entry selects are not read.

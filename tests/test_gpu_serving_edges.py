@@ -1,10 +1,11 @@
 """Rare paths of the token-score and cache-budget calls: what ordinary inputs
 seldom reach, each against a plain computation."""
-import numpy as np
+import ctypes
+
 import pytest
 import torch
 
-from ddtree_speculative_decode_b200 import lib, spec_engine, synth
+from ddtree_speculative_decode_b200 import build, lib, spec_engine, synth
 from test_gpu_logprobs import check
 
 DEV = "cuda:0"
@@ -166,3 +167,12 @@ def test_weights_with_the_loosest_bound(most, dtype, H, d):
         assert status.tolist() == [lib.DDT_OK] * B
         got.append(score)
     assert torch.equal(*got)
+
+
+def test_logprobs_entries_that_32_bits_cannot_count():
+    """Entry numbers are counted past the last one, by up to a launch's CTAs: refused before anything is launched."""
+    build.build()
+    p = ctypes.c_void_p(256)
+    for B, M in ((1, 2 ** 31 - 1), (2, 2 ** 30 - 100), (1, 2 ** 31 - 2 ** 16)):
+        assert lib.load().ddt_token_logprobs(p, 1, 8, 8, None, p, B, M, M, 0, p, None, None, None, None,
+                                             None) == lib.DDT_ERR_UNSUPPORTED
