@@ -115,8 +115,8 @@ int ddt_cache_weights(const void* q, const float* lse, const void* kv, int64_t k
   if (in_dtype != DDT_F32 && in_dtype != DDT_BF16) return DDT_ERR_INVALID_ARG;
   const uintptr_t elt = in_dtype == DDT_F32 ? 4 : 2;
   if (!ddt::aligned(q, elt) || !ddt::aligned(kv, elt)) return DDT_ERR_INVALID_ARG;
-  if (d_qk > 1024 || kv_rows > 0x7fffffffLL || (long long)B * N > 0x7fffffffLL / H ||
-      (nodes && (long long)M * H > 0x7fffffffLL))
+  if (d_qk > 1024 || kv_rows > 0x7fffffffLL || (long long)B * N > (ddt::kMaxRows - 1) / H ||
+      (nodes && (long long)M * H >= ddt::kMaxRows))
     return DDT_ERR_UNSUPPORTED;
   ddt::WeightsParams p{};
   p.q = q;

@@ -497,7 +497,8 @@ DDT_API int ddt_token_logprobs(const void* logits, int logits_dtype, int V, int6
  * Precondition the library cannot check: the requests own disjoint rows.
  * Errors: DDT_ERR_INVALID_ARG (nulls, sizes, dtype, scale not finite and
  *   positive, decay not finite, workspace), DDT_ERR_UNSUPPORTED (d_qk > 1024,
- *   pools or row counts of 2^31 and more), DDT_ERR_CUDA (launch).
+ *   pools of 2^31 rows, B * N * H or M * H of 2^31 - 2^16 and more),
+ *   DDT_ERR_CUDA (launch).
  */
 DDT_API size_t ddt_cache_weights_workspace_size(int B, int N, int H, int d_qk, int max_cache_len, int in_dtype);
 

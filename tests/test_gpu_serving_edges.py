@@ -176,3 +176,12 @@ def test_logprobs_entries_that_32_bits_cannot_count():
     for B, M in ((1, 2 ** 31 - 1), (2, 2 ** 30 - 100), (1, 2 ** 31 - 2 ** 16)):
         assert lib.load().ddt_token_logprobs(p, 1, 8, 8, None, p, B, M, M, 0, p, None, None, None, None,
                                              None) == lib.DDT_ERR_UNSUPPORTED
+
+
+def test_weights_rows_that_32_bits_cannot_count():
+    """As above, for (entry, head) rows, which the kernels take in tiles."""
+    build.build()
+    p = ctypes.c_void_p(256)
+    for N, M, H, nodes in ((2 ** 31 - 1, 0, 1, None), (2 ** 28 - 1, 0, 8, None), (100, 2 ** 28 - 1, 8, p)):
+        assert lib.load().ddt_cache_weights(p, p, p, 100, p, p, nodes, p, 1, N, M, H, 8, 0.1, 0, 50, 0, None, 1.0, p, None,
+                                            None, 0, None) == lib.DDT_ERR_UNSUPPORTED
