@@ -495,8 +495,9 @@ static int launch_select(const EvictParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, evict_select_kernel, p) == cudaSuccess ? DDT_OK : DDT_ERR_CUDA;
 }
 
+// The move's split; false: more CTAs than a launch may have.
 template <typename Tv>
-static int launch_move(EvictParams p, cudaStream_t stream) {
+static bool split_move(EvictParams& p) {
   p.row_vecs = p.row_bytes / (int)sizeof(Tv);
   const long long lbs = (long long)p.n_layers * p.B;
   if (p.kv_dst) {
@@ -511,8 +512,12 @@ static int launch_move(EvictParams p, cudaStream_t stream) {
     while (p.col * (int)sizeof(Tv) > 32 && lbs * ((p.row_vecs + p.col - 1) / p.col) < 4 * sm_count()) p.col >>= 1;
     p.blocks = (p.row_vecs + p.col - 1) / p.col + 1;  // and the scores
   }
-  if (lbs * p.blocks > 0x7fffffffLL) return DDT_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)(lbs * p.blocks);
+  return lbs * p.blocks <= 0x7fffffffLL;
+}
+
+template <typename Tv>
+static int launch_move(const EvictParams& p, cudaStream_t stream) {
+  const unsigned grid = (unsigned)p.n_layers * (unsigned)p.B * (unsigned)p.blocks;
   return p.kv_dst ? launch_pdl(evict_copy_kernel<Tv>, grid, kMoveThreads, 0, stream, p)
                   : launch_pdl(evict_shift_kernel<Tv>, grid, kMoveThreads, 0, stream, p);
 }
@@ -542,11 +547,12 @@ int launch_cache_evict(EvictParams p, int max_cache_len, void* workspace, cudaSt
   // one beyond what is set aside) re-reads its scores instead
   const int slice = (std::min(max_cache_len, kMaxLen) + p.cluster - 1) / p.cluster;
   p.held_keys = std::min(kSelKeys, (slice + 1023) / 1024 * 1024);
+  auto al = [](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
+  const bool wide = p.row_bytes % 16 == 0 && al(p.kv, 16) && al(p.kv_dst, 16);
+  if (!(wide ? split_move<uint4>(p) : split_move<uint32_t>(p))) return DDT_ERR_UNSUPPORTED;  // before anything is written
   const int st = launch_select(p, stream);
   if (st != DDT_OK) return st;
-  auto al = [](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
-  if (p.row_bytes % 16 == 0 && al(p.kv, 16) && al(p.kv_dst, 16)) return launch_move<uint4>(p, stream);
-  return launch_move<uint32_t>(p, stream);
+  return wide ? launch_move<uint4>(p, stream) : launch_move<uint32_t>(p, stream);
 }
 
 }  // namespace ddt

@@ -185,3 +185,13 @@ def test_weights_rows_that_32_bits_cannot_count():
     for N, M, H, nodes in ((2 ** 31 - 1, 0, 1, None), (2 ** 28 - 1, 0, 8, None), (100, 2 ** 28 - 1, 8, p)):
         assert lib.load().ddt_cache_weights(p, p, p, 100, p, p, nodes, p, 1, N, M, H, 8, 0.1, 0, 50, 0, None, 1.0, p, None,
                                             None, 0, None) == lib.DDT_ERR_UNSUPPORTED
+
+
+def test_evict_refuses_before_it_selects():
+    """More CTAs than a launch may have for the move: refused before the selection writes statuses and lists that no
+    move follows."""
+    build.build()
+    p, q = ctypes.c_void_p(256), ctypes.c_void_p(1 << 20)
+    for kd, rows, B, mk in ((q, 100, 64, 1 << 30), (None, 0, 1 << 20, 8)):  # copied, in place; rows of 1 MB
+        assert lib.load().ddt_cache_evict(p, 100, 0, 1 << 18, p, 1, 0, p, p, p, 0, 0, B, 50, kd, rows, kd, 0, kd, p, p, mk,
+                                          None, p, 1 << 40, None) == lib.DDT_ERR_UNSUPPORTED
